@@ -75,10 +75,13 @@ typedef enum {
   LRMOE_EPI_SWIGLU_BWD = 1   /* out = [dG | dU] from dA = rows . W[e] and saved g, u */
 } lrmoe_epilogue;
 
+/* Score of lrmoe_route: how a router logit becomes a routing weight. */
+typedef enum { LRMOE_SCORE_SOFTMAX = 0, LRMOE_SCORE_SIGMOID = 1 } lrmoe_score_fn;
+
 /* Device status word bits. */
 #define LRMOE_ST_BAD_EXPERT 1u /* some topk_idx >= E (that pair was skipped) */
 #define LRMOE_ST_BAD_QUOTA  2u /* some quota < 0 (treated as 0) */
-#define LRMOE_ST_NONFINITE  4u /* some score was +Inf or NaN */
+#define LRMOE_ST_NONFINITE  4u /* some score, router logit or router bias was +Inf or NaN */
 #define LRMOE_ST_TIMEOUT    8u /* a bounded device-side wait gave up; outputs invalid */
 #define LRMOE_ST_BAD_INDEX 16u /* an index (perm/pos entry; checked build: any) was out of range; skipped */
 
@@ -455,6 +458,116 @@ int lrmoe_grouped_dgrad_wgrad(const void* grad_rows, int rows_cap, const void* W
  * ------------------------------------------------------------------------- */
 int lrmoe_unpack(const void* dXp, int rows_cap, const int32_t* pos, int T, int k, int H,
                  lrmoe_dtype dt, void* dX, uint32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The layer's forward, up to the tensors that the backward takes.  RU-B bullet
+ * 1, FR-B bullet 1, DE paragraph 3: the forward computes every routed pair.  The
+ * pages start from routed pairs and saved tensors and describe neither router
+ * nor forward kernels; the formulas below are those of the layer in this
+ * header's notation.  A forward that keeps every pair runs
+ *   lrmoe_route -> lrmoe_quota_controller(cap 0, max_pairs -1: quota = counts) ->
+ *   lrmoe_select_quota(score = topk_w) -> lrmoe_grouped_swiglu ->
+ *   lrmoe_grouped_linear -> lrmoe_combine,
+ * and leaves topk_idx, topk_w, g, u, a in the layouts of lrmoe_pruned_backward
+ * and y in that of lrmoe_router_grad.  None of these calls keeps any state
+ * between launches.
+ *
+ * lrmoe_route: experts and weights of every token from router logits
+ * z [T][E] in dtype dt (rows contiguous; E need not be a multiple of 8).
+ *   s = softmax(z) over the token's experts, or sigmoid(z)
+ *   selection key c_e = s_e + bias[e] (bias [E] fp32, may be NULL; it steers the
+ *     selection only and gets no gradient)
+ *   the E experts are n_group runs of E / n_group; a group's value is the sum of
+ *     its two largest keys (of one, if one expert of it is available); the
+ *     topk_group groups of largest value stay (n_group = 1: all)
+ *   the k largest keys among them, in descending order, become slots 0..k-1
+ *   topk_w = scale * s_e, with renormalise != 0 scale * s_e / sum of the chosen s
+ * Ties go to the lower group and the lower expert.  Keys are compared as
+ * computed in fp64 (without bias experts are ordered by their logits);
+ * weights are fp32.  A logit of -Inf takes the expert out for that token (its
+ * score is 0), a bias of -Inf for all tokens (the softmax still counts it).  The
+ * lowest finite number is not -Inf: such an expert has a score of (nearly) 0 but
+ * can be chosen, also by its bias.  NaN and +Inf, in logits or bias,
+ * count as -Inf and set LRMOE_ST_NONFINITE.  Slots without an expert (fewer than
+ * k available) get topk_idx -1 and topk_w +0.  Limits: k <= 32, k <= E <= 1024,
+ * n_group <= 32 and a divisor of E, k <= topk_group * E / n_group; scale finite.
+ *
+ * lrmoe_route_grad: dlogits [T][E] in dtype dt from dw [T*k] fp32, the gradient
+ * of topk_w (lrmoe_router_grad; a dropped pair's dw is 0), for the same logits
+ * and settings and any topk_idx [T*k] (the selection is taken as it is; an
+ * expert named twice counts twice).  With d_j = scale * dw_j, S = sum of the
+ * slots' s:  renormalised d_j <- (d_j - sum_i d_i s_i / S) / S;  D_e = sum of d_j
+ * over the slots of e;  softmax dz_e = s_e (D_e - sum_f D_f s_f), sigmoid
+ * dz_e = D_e s_e (1 - s_e).  Sums in fp32, one rounding to dt.  Empty slots are
+ * skipped (dw not read); ids >= E likewise and set LRMOE_ST_BAD_EXPERT; a slot
+ * whose logit is not finite is skipped, and experts with such logits get 0
+ * (NaN and +Inf set LRMOE_ST_NONFINITE where they are read: every logit with
+ * softmax and renormalise == 0, else the slots').  dlogits must not overlap an
+ * input.
+ * ------------------------------------------------------------------------- */
+int lrmoe_route(const void* logits, int T, int E, lrmoe_dtype dt, const float* bias, int k,
+                lrmoe_score_fn score_fn, int n_group, int topk_group, int renormalise, float scale,
+                int32_t* topk_idx, float* topk_w, uint32_t* status, void* stream);
+int lrmoe_route_grad(const void* logits, int T, int E, lrmoe_dtype dt, const int32_t* topk_idx,
+                     int k, lrmoe_score_fn score_fn, int renormalise, float scale, const float* dw,
+                     void* dlogits, uint32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The experts' forward products (see above; offsets and packed rows as in
+ * lrmoe_grouped_dgrad, weights as the layer stores them, accumulation in fp32,
+ * each output rounded once).
+ *
+ * lrmoe_grouped_swiglu: for packed rows r of expert e
+ *   [g_r | u_r] = x_r . W_gu[e]^T + bias[e],   a_r = silu(g_r) * u_r
+ *   W_gu [E][2I][H], bias [E][2I] in dt or NULL (none).
+ *   With perm, r stands for pair p = perm[r] (lrmoe_select_quota): x_r =
+ *   x[p / src_div] (x [n_src][H], src_div = k for token rows; p must lie in
+ *   [0, n_src*src_div)), read in place, and g, u, a [n_src*src_div][I] are
+ *   written at row p.  Without perm (NULL) x holds the packed rows (n_src >=
+ *   rows_cap, src_div = 1) and g, u, a [rows_cap][I] are written at row r.
+ *   Ap [rows_cap][I] gets a_r at row r in either case (the next product's
+ *   rows).  g, u, a may each be NULL (not written).
+ * lrmoe_grouped_linear: out[o] = rows[r] . W[e]^T + bias[e] + residual[o] with
+ *   o = perm[r] in [0, n_out), or r without perm (n_out >= rows_cap);
+ *   rows [rows_cap][K], W [E][N][K], bias [E][N] and residual [n_out][N] in dt,
+ *   each or both NULL (none).  residual may be out itself.  With E = 1 and
+ *   offsets = {0, rows} it is a plain linear layer (a shared expert).
+ * lrmoe_grouped_bias_grad: db[e][n] = sum of grad_rows[r][n] over r in R_e
+ *   (grad_rows [rows_cap][N] in dt: dGUp for the bias of W_gu, DYp for that of
+ *   W_down), db [E][N] fp32, zeros for an empty expert; accumulate = 1 adds to
+ *   db.  fp32 sums in a fixed order.
+ *
+ * perm entries out of range set LRMOE_ST_BAD_INDEX and that row's outputs are
+ * left unwritten; perm must not name a row twice.  Output rows that no packed
+ * row names are left as they were.  Apart from residual = out, outputs must not
+ * overlap inputs or one another.  E <= 1024.
+ * ------------------------------------------------------------------------- */
+int lrmoe_grouped_swiglu(const void* x, int n_src, int src_div, const int32_t* perm,
+                         const int32_t* offsets, int rows_cap, const void* W_gu, const void* bias,
+                         int E, int H, int I, lrmoe_dtype dt, void* Ap, void* g, void* u, void* a,
+                         uint32_t* status, void* stream);
+int lrmoe_grouped_linear(const void* rows, int rows_cap, const void* W, const void* bias,
+                         const int32_t* offsets, int E, int K, int N, lrmoe_dtype dt,
+                         const void* residual, const int32_t* perm, int n_out, void* out,
+                         uint32_t* status, void* stream);
+int lrmoe_grouped_bias_grad(const void* grad_rows, int rows_cap, const int32_t* offsets, int E,
+                            int N, lrmoe_dtype dt, float* db, int accumulate, uint32_t* status,
+                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The layer output (see above):
+ *
+ *   Y[t] = RNE_dt( sum_{j ascending, topk_idx[t*k+j] >= 0} topk_w[t*k+j] * y[t*k+j] + residual[t] )
+ *
+ * y [T*k][H] (pair order, rows of empty slots not read), Y and residual [T][H]
+ * in dt; residual may be NULL (none) or Y itself.  fp32 fused multiply-adds in
+ * slot order, one rounding.  ids >= E are skipped and set LRMOE_ST_BAD_EXPERT.
+ * Its gradient is what the path already has: w * dY (lrmoe_pack), <dY, y>
+ * (lrmoe_router_grad), and dY itself for the residual.
+ * ------------------------------------------------------------------------- */
+int lrmoe_combine(const void* y, const int32_t* topk_idx, const float* topk_w, int T, int k, int E,
+                  int H, lrmoe_dtype dt, const void* residual, void* Y, uint32_t* status,
+                  void* stream);
 
 /* ---------------------------------------------------------------------------
  * The whole path a1..a5 on one stream (RU-B bullets 3-5): score, selection,

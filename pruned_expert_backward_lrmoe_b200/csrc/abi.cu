@@ -48,6 +48,10 @@ static int elem_multiple(lrmoe_dtype dt) { return dt == LRMOE_BF16 ? 8 : 4; }
 
 static bool valid_dtype(lrmoe_dtype dt) { return dt == LRMOE_F32 || dt == LRMOE_BF16; }
 
+static bool valid_score_fn(lrmoe_score_fn f) {
+  return f == LRMOE_SCORE_SOFTMAX || f == LRMOE_SCORE_SIGMOID;
+}
+
 #define REQUIRE(cond, ...)                                 \
   do {                                                     \
     if (!(cond)) return fail(LRMOE_ERR_INVALID_ARG, __VA_ARGS__); \
@@ -507,6 +511,151 @@ int lrmoe_grouped_dgrad_wgrad(const void* grad_rows, int rows_cap, const void* W
                                         in_rows, N2, dW, accumulate, status,
                                         static_cast<cudaStream_t>(stream), &why);
   return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, why);
+}
+
+int lrmoe_route(const void* logits, int T, int E, lrmoe_dtype dt, const float* bias, int k,
+                lrmoe_score_fn score_fn, int n_group, int topk_group, int renormalise, float scale,
+                int32_t* topk_idx, float* topk_w, uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  REQUIRE(valid_score_fn(score_fn), "unknown score function %d", (int)score_fn);
+  if (int r = check_pairs(T, k, E)) return r;
+  if (E > kMaxGroupedExperts) return fail(LRMOE_ERR_UNSUPPORTED, "E=%d > %d", E, kMaxGroupedExperts);
+  REQUIRE(k <= E, "k=%d > E=%d", k, E);
+  REQUIRE(n_group > 0 && E % n_group == 0, "n_group=%d must divide E=%d", n_group, E);
+  if (n_group > 32) return fail(LRMOE_ERR_UNSUPPORTED, "n_group=%d > 32", n_group);
+  REQUIRE(topk_group > 0 && topk_group <= n_group, "topk_group=%d must be in [1, %d]", topk_group,
+          n_group);
+  REQUIRE(k <= topk_group * (E / n_group), "k=%d > the %d experts of topk_group=%d groups", k,
+          topk_group * (E / n_group), topk_group);
+  REQUIRE(scale - scale == 0.0f, "scale must be finite");
+  REQUIRE_PTR(logits);
+  REQUIRE(bias == nullptr || aligned16(bias), "bias is not 16-byte aligned");
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(topk_w);
+  cudaError_t e = launch_route(logits, T, E, dt, bias, k, score_fn, n_group, topk_group,
+                               renormalise != 0, scale, topk_idx, topk_w, status,
+                               static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_route launch");
+}
+
+int lrmoe_route_grad(const void* logits, int T, int E, lrmoe_dtype dt, const int32_t* topk_idx,
+                     int k, lrmoe_score_fn score_fn, int renormalise, float scale, const float* dw,
+                     void* dlogits, uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  REQUIRE(valid_score_fn(score_fn), "unknown score function %d", (int)score_fn);
+  if (int r = check_pairs(T, k, E)) return r;
+  if (E > kMaxGroupedExperts) return fail(LRMOE_ERR_UNSUPPORTED, "E=%d > %d", E, kMaxGroupedExperts);
+  REQUIRE(scale - scale == 0.0f, "scale must be finite");
+  REQUIRE_PTR(logits);
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(dw);
+  REQUIRE_PTR(dlogits);
+  REQUIRE(dlogits != logits, "dlogits must not be logits");
+  cudaError_t e = launch_route_grad(logits, T, E, dt, topk_idx, k, score_fn, renormalise != 0, scale,
+                                    dw, dlogits, status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_route_grad launch");
+}
+
+int lrmoe_grouped_swiglu(const void* x, int n_src, int src_div, const int32_t* perm,
+                         const int32_t* offsets, int rows_cap, const void* W_gu, const void* bias,
+                         int E, int H, int I, lrmoe_dtype dt, void* Ap, void* g, void* u, void* a,
+                         uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  REQUIRE(E > 0 && rows_cap > 0 && n_src > 0, "E, rows_cap and n_src must be positive");
+  if (E > kMaxGroupedExperts) return fail(LRMOE_ERR_UNSUPPORTED, "E=%d > %d", E, kMaxGroupedExperts);
+  REQUIRE(src_div > 0 && (perm != nullptr || src_div == 1),
+          "src_div=%d must be positive, and 1 without perm", src_div);
+  REQUIRE((long long)n_src * src_div < (1LL << 31) - 1, "n_src*src_div overflows int32");
+  REQUIRE(perm != nullptr || n_src >= rows_cap, "n_src=%d < rows_cap=%d without perm", n_src,
+          rows_cap);
+  if (int r = check_feature(H, dt, "H")) return r;
+  if (int r = check_feature(I, dt, "I")) return r;
+  REQUIRE_PTR(x);
+  REQUIRE(perm == nullptr || aligned16(perm), "perm is not 16-byte aligned");
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(W_gu);
+  REQUIRE(bias == nullptr || aligned16(bias), "bias is not 16-byte aligned");
+  REQUIRE_PTR(Ap);
+  REQUIRE(aligned16(g) && aligned16(u) && aligned16(a), "g, u or a is not 16-byte aligned");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dt == LRMOE_BF16) {
+    const char* why = "lrmoe_grouped_swiglu launch";
+    cudaError_t e = launch_swiglu_tc(x, n_src, src_div, perm, offsets, rows_cap, W_gu, bias, E, H, I,
+                                     Ap, g, u, a, status, s, &why);
+    return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, why);
+  }
+  cudaError_t e = launch_swiglu_simt(x, n_src, src_div, perm, offsets, rows_cap, W_gu, bias, E, H, I,
+                                     Ap, g, u, a, status, s);
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_grouped_swiglu launch");
+}
+
+int lrmoe_grouped_linear(const void* rows, int rows_cap, const void* W, const void* bias,
+                         const int32_t* offsets, int E, int K, int N, lrmoe_dtype dt,
+                         const void* residual, const int32_t* perm, int n_out, void* out,
+                         uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  REQUIRE(E > 0 && rows_cap > 0 && n_out > 0, "E, rows_cap and n_out must be positive");
+  if (E > kMaxGroupedExperts) return fail(LRMOE_ERR_UNSUPPORTED, "E=%d > %d", E, kMaxGroupedExperts);
+  REQUIRE(perm != nullptr || n_out >= rows_cap, "n_out=%d < rows_cap=%d without perm", n_out,
+          rows_cap);
+  if (int r = check_feature(K, dt, "K")) return r;
+  if (int r = check_feature(N, dt, "N")) return r;
+  REQUIRE_PTR(rows);
+  REQUIRE_PTR(W);
+  REQUIRE(bias == nullptr || aligned16(bias), "bias is not 16-byte aligned");
+  REQUIRE_PTR(offsets);
+  REQUIRE(residual == nullptr || aligned16(residual), "residual is not 16-byte aligned");
+  REQUIRE(perm == nullptr || aligned16(perm), "perm is not 16-byte aligned");
+  REQUIRE_PTR(out);
+  REQUIRE(out != rows, "out must not be rows");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dt == LRMOE_BF16) {
+    const char* why = "lrmoe_grouped_linear launch";
+    cudaError_t e = launch_linear_tc(rows, rows_cap, W, bias, offsets, E, K, N, residual, perm, n_out,
+                                     out, status, s, &why);
+    return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, why);
+  }
+  cudaError_t e = launch_linear_simt(rows, rows_cap, W, bias, offsets, E, K, N, residual, perm, n_out,
+                                     out, status, s);
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_grouped_linear launch");
+}
+
+int lrmoe_grouped_bias_grad(const void* grad_rows, int rows_cap, const int32_t* offsets, int E,
+                            int N, lrmoe_dtype dt, float* db, int accumulate, uint32_t* status,
+                            void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  REQUIRE(E > 0 && rows_cap > 0, "E and rows_cap must be positive");
+  if (E > kMaxGroupedExperts) return fail(LRMOE_ERR_UNSUPPORTED, "E=%d > %d", E, kMaxGroupedExperts);
+  if (int r = check_feature(N, dt, "N")) return r;
+  REQUIRE_PTR(grad_rows);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(db);
+  cudaError_t e = launch_bias_grad(grad_rows, rows_cap, offsets, E, N, dt, db, accumulate != 0,
+                                   status, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_grouped_bias_grad launch");
+}
+
+int lrmoe_combine(const void* y, const int32_t* topk_idx, const float* topk_w, int T, int k, int E,
+                  int H, lrmoe_dtype dt, const void* residual, void* Y, uint32_t* status,
+                  void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  if (int r = check_pairs(T, k, E)) return r;
+  if (int r = check_feature(H, dt, "H")) return r;
+  REQUIRE_PTR(y);
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(topk_w);
+  REQUIRE(residual == nullptr || aligned16(residual), "residual is not 16-byte aligned");
+  REQUIRE_PTR(Y);
+  REQUIRE(Y != y, "Y must not be y");
+  cudaError_t e = launch_combine(y, topk_idx, topk_w, T, k, E, H, dt, residual, Y, status,
+                                 static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_combine launch");
 }
 
 int lrmoe_gather_rows(const void* src, int n_src, int row_bytes, const int32_t* idx, int n,

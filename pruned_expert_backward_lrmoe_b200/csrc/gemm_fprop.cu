@@ -1,0 +1,561 @@
+// The experts' forward products for bf16 storage: variable-size grouped GEMMs against
+// K-major weights, with the bias, the SwiGLU activation, the residual and the scatter to
+// pair order in the epilogue.
+//
+//   SwiGLU: [g | u] = x_r . W_gu[e]^T + b[e],  a = silu(g) * u      (x_r gathered by perm)
+//   linear: out     = rows_r . W[e]^T + b[e] + residual
+//
+// The expert feed-forward g = x W_gate^T, u = x W_up^T, a = silu(g) * u, y = a W_down^T is
+// what the pruned backward of "LRMoE урезает обратный проход MoE ..." (section "Что делает
+// LRMoE", bullet 1: the forward computes every pair) takes its saved tensors from.
+//
+// Mathematics: D = A . B^T with A = the expert's rows [m][K] and B = the expert's weights
+// [N][K], both K-major, so A and B are staged alike: 64-deep K blocks as 128-byte rows under
+// the 128-byte swizzle.  The accumulators stay in fp32 in tensor memory; bias, activation and
+// residual are applied to the fp32 values and each output is rounded once, to bf16 (the stored
+// g and u are rounded copies: a is formed from the unrounded ones).
+//
+// Tiles.  PAIR: a cluster of two CTAs shares one tcgen05.mma.cta_group::2 of 256 rows x 256
+// columns; each CTA stages its 128 rows of A and 128 of the 256 rows of B.  One SM: 128 rows x
+// 256 columns.  For SwiGLU the 256 columns are 128 gate rows and the 128 up rows of the same
+// features, so that a thread finds g and u of a feature in its own tensor-memory lane and the
+// activation needs no exchange.  An expert's rows go to PAIR tiles, a last tile of at most 128
+// rows to a one-SM tile in a second launch that overlaps the first one's drain.
+//
+// Every tile has the same K depth, so tiles are dealt out in turn; there is no device-side
+// scheduling state that two launches or two captured graphs could share.
+//
+// Roles (320 threads): warp 0 producer (TMA; with perm, its 32 lanes each fetch four gathered
+// rows per K block), warp 1 tensor memory and MMA issue, warps 2-9 epilogue.  Every wait is
+// bounded (LRMOE_ST_TIMEOUT, then a clean exit).  No TMA multicast.
+#include "gemm_common.cuh"
+
+namespace lrmoe {
+namespace {
+
+struct FpropParams {
+  const int32_t* offsets;
+  int E, K, N;              // N: output features (SwiGLU: I)
+  const int32_t* perm;      // packed row -> pair (nullptr: identity)
+  int gather;               // A rows are gathered: packed row r reads source row perm[r] / src_div
+  int src_div;
+  int n_out;                // rows of the pair-order outputs
+  const uint16_t* bias;     // [E][N] (SwiGLU: [E][2N]) or nullptr
+  const uint16_t* residual; // linear: [n_out][N] or nullptr
+  uint16_t* out;            // linear: [n_out][N]; SwiGLU: packed a [rows_cap][N]
+  uint16_t* g;              // SwiGLU, each optional: pair-order [n_out][N]
+  uint16_t* u;
+  uint16_t* a;
+  uint32_t* status;
+  int part;                 // RowPart
+  int late_wait;
+  int rows_cap;
+};
+
+template <bool PAIR>
+struct FwdLayout {
+  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr int kABytes = BM * BK * 2;                       // 16 KB
+  static constexpr int kBBytes = (PAIR ? kBNT / 2 : kBNT) * BK * 2; // 16 KB / 32 KB
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kBarOff = kStages * kStageBytes;
+  static constexpr int kNumBars = 2 * kStages + 5;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  static constexpr int kTableOff = kMiscOff + 16;
+  __host__ __device__ static constexpr int table_ints(int E) { return 2 * (E + 1) + 33; }
+  __host__ __device__ static constexpr int alloc(int E) {
+    return kTableOff + table_ints(E) * 4 + 1024;
+  }
+};
+
+struct FwdTile {
+  int e, row0, row_end, n0;
+};
+
+template <bool SWIGLU, bool PAIR>
+__device__ __forceinline__ FwdTile decode_fwd(int t, const FpropParams& p, const int* offs,
+                                              const int* tab, int nt) {
+  constexpr int kFeat = SWIGLU ? kBNT / 2 : kBNT;
+  FwdTile ti;
+  ti.e = find_group(tab, p.E, t);
+  const int local = t - tab[ti.e];
+  ti.n0 = (local % nt) * kFeat;
+  ti.row0 = dgrad_tile_row0(offs[ti.e], offs[ti.e + 1] - offs[ti.e], PAIR ? 2 * BM : BM, p.part,
+                            local / nt);
+  ti.row_end = offs[ti.e + 1];
+  return ti;
+}
+
+// Four gathered rows (64 bf16 columns from c0) of a row-major matrix, box of one row.
+__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, uint64_t* bar, int c0,
+                                            const int (&r)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(r[0]), "r"(r[1]),
+      "r"(r[2]), "r"(r[3])
+      : "memory");
+}
+
+// The same with completion counted on a barrier of either CTA of the pair (cluster address).
+__device__ __forceinline__ void tma_gather4_pair(void* dst, const void* tmap, uint32_t bar_cl,
+                                                 int c0, const int (&r)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cl), "r"(c0), "r"(r[0]), "r"(r[1]),
+      "r"(r[2]), "r"(r[3])
+      : "memory");
+}
+
+// 32 values of columns [nb, nb + 32) added to r (columns >= N skipped; N % 8 == 0).  Plain
+// loads: the residual may be the output itself.
+__device__ __forceinline__ void add_row32(uint32_t (&r)[32], const uint16_t* v, int nb, int N) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (nb + c * 8 < N) {
+      const uint4 w = *reinterpret_cast<const uint4*>(v + nb + c * 8);
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[8 * c + 2 * i] = __float_as_uint(__uint_as_float(r[8 * c + 2 * i]) +
+                                           bf16_bits_to_f32(h[i] & 0xffffu));
+        r[8 * c + 2 * i + 1] = __float_as_uint(__uint_as_float(r[8 * c + 2 * i + 1]) +
+                                               bf16_bits_to_f32(h[i] >> 16));
+      }
+    }
+  }
+}
+
+template <bool SWIGLU, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
+    const __grid_constant__ CUtensorMap tmA /* rows: 32-row boxes, or one-row boxes to gather */,
+    const __grid_constant__ CUtensorMap tmB /* W [E][rows][K], 128-row boxes */,
+    const FpropParams p) {
+  using L = FwdLayout<PAIR>;
+  constexpr int STAGES = L::kStages;
+  constexpr int BN = kBNT;
+  constexpr int kTileM = PAIR ? 2 * BM : BM;
+  const int E = p.E;
+  uint32_t* status = p.status;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBarOff);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + STAGES;
+  uint64_t* tfull = bars + 2 * STAGES;       // [2]
+  uint64_t* tempty = bars + 2 * STAGES + 2;  // [2]
+  uint64_t* mma_done = bars + 2 * STAGES + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+  int* tab = reinterpret_cast<int*>(smem + L::kTableOff);
+  int* offs_s = tab + (E + 1);
+  int* scratch = offs_s + (E + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;
+  const bool leader = rank == 0;
+  const int first = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+  const int step = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], PAIR ? 2 : 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], (PAIR ? 2 : 1) * kEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, 2 * BN);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 2 * BN);
+      tmem_relinquish();
+    }
+  }
+  if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers exist before any remote arrival
+  // A late-wait launch (the last tiles of the experts, behind the PAIR launch of the same
+  // product) reads only what was complete when that launch started.
+  if (!p.late_wait) {
+    pdl_wait();
+    pdl_trigger();
+  }
+  const int nt = (p.N + (SWIGLU ? BN / 2 : BN) - 1) / (SWIGLU ? BN / 2 : BN);
+  int total = build_dgrad_tiles(p.offsets, E, kTileM, nt, tab, scratch, p.part);
+  for (int i = threadIdx.x; i <= E; i += blockDim.x) offs_s[i] = p.offsets[i];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (offsets_invalid(offs_s, E, p.rows_cap, status)) total = 0;
+  const uint32_t tmem_base = *tmem_slot;
+  const int nk = (p.K + BK - 1) / BK;
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t armed = 0, armed_par = 0;
+    const uint32_t lead_full = PAIR ? cluster_addr(full, 0) : 0u;
+    bool ok = true;
+    for (int t = first; t < total && ok; t += step) {
+      const FwdTile ti = decode_fwd<SWIGLU, PAIR>(t, p, offs_s, tab, nt);
+      const int base = ti.row0 + rank * BM;  // this CTA's first row
+      // Row groups of A with at least one of the expert's rows are loaded; what shared memory
+      // holds in the others only reaches accumulator rows that are never stored.
+      const int unit = p.gather ? 4 : 32;
+      auto groups = [&](int b) {
+        int n = ti.row_end - b;
+        n = n < 0 ? 0 : (n > BM ? BM : n);
+        return (n + unit - 1) / unit;
+      };
+      const int mine = groups(base);
+      const uint32_t a_unit = (uint32_t)unit * BK * 2;
+      const uint32_t bytes =
+          (uint32_t)mine * a_unit + L::kBBytes +
+          (PAIR ? (uint32_t)groups(ti.row0 + BM) * a_unit + L::kBBytes : 0u);
+      int src[4] = {0, 0, 0, 0};
+      if (p.gather && lane < mine) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = base + lane * 4 + i;
+          const int pr = r < ti.row_end ? __ldg(p.perm + r) : 0;
+          // an entry out of range reads row 0; the epilogue flags it and stores nothing
+          src[i] = pr >= 0 && pr < p.n_out ? pr / p.src_div : 0;
+        }
+      }
+      const int brow = SWIGLU ? (rank ? p.N + ti.n0 : ti.n0) : ti.n0 + rank * (BN / 2);
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!__all_sync(kFull, mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, status))) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + stage * L::kStageBytes;
+        uint8_t* sb = sa + L::kABytes;
+        if (leader) {
+          if (lane == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+          armed |= 1u << stage;
+          armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+          __syncwarp();
+          if (lane < mine) {
+            if (p.gather)
+              tma_gather4(sa + lane * a_unit, &tmA, &full[stage], kb * BK, src);
+            else
+              tma_load_2d(sa + lane * a_unit, &tmA, &full[stage], kb * BK, base + lane * 32);
+          }
+          if (lane == 0) {
+            tma_load_3d(sb, &tmB, &full[stage], kb * BK, brow, ti.e);
+            if constexpr (!PAIR)
+              tma_load_3d(sb + L::kBBytes / 2, &tmB, &full[stage], kb * BK,
+                          SWIGLU ? p.N + ti.n0 : ti.n0 + BN / 2, ti.e);
+          }
+        } else {
+          const uint32_t fb = lead_full + 8u * stage;
+          if (lane < mine) {
+            if (p.gather)
+              tma_gather4_pair(sa + lane * a_unit, &tmA, fb, kb * BK, src);
+            else
+              tma_load_2d_pair(sa + lane * a_unit, &tmA, fb, kb * BK, base + lane * 32);
+          }
+          __syncwarp();
+          if (lane == 0) {
+            tma_load_3d_pair(sb, &tmB, fb, kb * BK, brow, ti.e);
+            mbar_arrive_cluster_relaxed(fb);  // the bytes are counted by the barrier itself
+          }
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // every load that was started lands before shared memory is released (the leader's
+    // barriers count the peer's bytes too)
+    if (leader && lane == 0)
+      for (int i = 0; i < STAGES; ++i)
+        if ((armed >> i) & 1u) mbar_wait_drain<PAIR>(&full[i], (armed_par >> i) & 1u);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t idesc = idesc_bf16_f32(kTileM, BN, false, false);
+      const uint32_t peer_empty = PAIR ? cluster_addr(empty, 1) : 0u;
+      const uint32_t peer_tfull = PAIR ? cluster_addr(tfull, 1) : 0u;
+      int stage = 0;
+      uint32_t phase = 0, acc_iter = 0;
+      bool ok = true;
+      for (int t = first; t < total && ok; t += step) {
+        const uint32_t b = acc_iter & 1u, bphase = (acc_iter >> 1) & 1u;
+        if (!__all_sync(kFull, mbar_wait_bounded(&tempty[b], bphase ^ 1u, abort_flag, status)))
+          break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + b * BN;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!__all_sync(kFull, mbar_wait_bounded(&full[stage], phase, abort_flag, status))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t a_addr = smem_u32(smem + stage * L::kStageBytes);
+            const uint32_t b_addr = a_addr + L::kABytes;
+#pragma unroll
+            for (int kk = 0; kk < BK / UK; ++kk) {
+              const uint64_t adesc = smem_desc_sw128(a_addr + kk * 32, 16, 1024);
+              const uint64_t bdesc = smem_desc_sw128(b_addr + kk * 32, 16, 1024);
+              if constexpr (PAIR)
+                tc_mma_f16_pair(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
+              else
+                tc_mma_f16(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
+            }
+            if constexpr (PAIR) {
+              tc_commit_pair(smem_u32(&empty[stage]));
+              tc_commit_pair(peer_empty + 8u * stage);
+            } else {
+              tc_commit(&empty[stage]);
+            }
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          if constexpr (PAIR) {
+            tc_commit_pair(smem_u32(&tfull[b]));
+            tc_commit_pair(peer_tfull + 8u * b);
+          } else {
+            tc_commit(&tfull[b]);
+          }
+        }
+        __syncwarp();
+        ++acc_iter;
+      }
+      // every issued MMA has finished before tensor memory is released
+      if (lane == 0) {
+        if constexpr (PAIR)
+          tc_commit_pair(smem_u32(mma_done));
+        else
+          tc_commit(mma_done);
+      }
+      __syncwarp();
+      mbar_wait_drain(mma_done, 0);
+    }
+  } else {
+    // ---------------- epilogue ----------------
+    const int ew = warp - 2;
+    const int q = warp & 3, half = ew >> 2;
+    const int row_in_tile = rank * BM + q * 32 + lane;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
+    const uint32_t lead_tempty = PAIR ? cluster_addr(tempty, 0) : 0u;
+    uint32_t acc_iter = 0;
+    auto release_acc = [&](uint32_t b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_remote(lead_tempty + 8u * b);
+        else
+          mbar_arrive(&tempty[b]);
+      }
+    };
+    for (int t = first; t < total; t += step) {
+      const FwdTile ti = decode_fwd<SWIGLU, PAIR>(t, p, offs_s, tab, nt);
+      const int row = ti.row0 + row_in_tile;
+      bool row_ok = row < ti.row_end;
+      int orow = row;
+      if (row_ok && p.perm != nullptr) {
+        orow = __ldg(p.perm + row);
+        if (orow < 0 || orow >= p.n_out) {
+          raise_status(status, LRMOE_ST_BAD_INDEX);
+          row_ok = false;
+        }
+      }
+      const uint32_t b = acc_iter & 1u, bphase = (acc_iter >> 1) & 1u;
+      if (!__all_sync(kFull, mbar_wait_bounded(&tfull[b], bphase, abort_flag, status))) break;
+      tc_fence_after();
+      if constexpr (SWIGLU) {
+        const uint16_t* bias = p.bias ? p.bias + (size_t)ti.e * 2 * p.N : nullptr;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int f = half * 64 + c * 32;  // feature inside the tile
+          const int nb = ti.n0 + f;
+          uint32_t rg[32], ru[32];
+          tmem_ld_32x32b_x32(lane_base + b * BN + f, rg);
+          tmem_ld_32x32b_x32(lane_base + b * BN + BN / 2 + f, ru);
+          tmem_wait_ld();
+          reg_fence(rg);
+          reg_fence(ru);
+          if (c == 1) release_acc(b);
+          if (row_ok && nb < p.N) {
+            if (bias) {
+              add_row32(rg, bias, nb, p.N);
+              add_row32(ru, bias + p.N, nb, p.N);
+            }
+            const size_t at = (size_t)orow * p.N;
+            if (p.g) epi_store_bf16(rg, p.g + at, nb, p.N);
+            if (p.u) epi_store_bf16(ru, p.u + at, nb, p.N);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float g = __uint_as_float(rg[i]);
+              rg[i] = __float_as_uint(g * sigmoid_fast(g) * __uint_as_float(ru[i]));
+            }
+            if (p.a) epi_store_bf16(rg, p.a + at, nb, p.N);
+            epi_store_bf16(rg, p.out + (size_t)row * p.N, nb, p.N);
+          }
+        }
+      } else {
+        const uint16_t* bias = p.bias ? p.bias + (size_t)ti.e * p.N : nullptr;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = half * 128 + c * 32;
+          const int nb = ti.n0 + col;
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(lane_base + b * BN + col, r);
+          tmem_wait_ld();
+          reg_fence(r);
+          if (c == 3) release_acc(b);
+          if (row_ok && nb < p.N) {
+            const size_t at = (size_t)orow * p.N;
+            if (bias) add_row32(r, bias, nb, p.N);
+            if (p.residual) add_row32(r, p.residual + at, nb, p.N);
+            epi_store_bf16(r, p.out + at, nb, p.N);
+          }
+        }
+      }
+      ++acc_iter;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) {
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, 2 * BN);
+    else
+      tmem_dealloc(tmem_base, 2 * BN);
+  }
+  if (p.late_wait) {
+    // this grid completes only after the kernel before it, so the next kernel in the
+    // stream sees both launches' rows
+    pdl_wait();
+    pdl_trigger();
+  }
+}
+
+template <bool SWIGLU, bool PAIR>
+cudaError_t launch_fprop(const CUtensorMap& a, const CUtensorMap& b, FpropParams prm,
+                         cudaStream_t s) {
+  using L = FwdLayout<PAIR>;
+  const int smem = L::alloc(prm.E);
+  if (smem > kSmemLimit) return cudaErrorInvalidConfiguration;
+  auto kern = fprop_kernel<SWIGLU, PAIR>;
+  // set on every launch (host-side only): a cached flag would go stale when the device's
+  // context is reset
+  cudaError_t err =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  if (err != cudaSuccess) return err;
+  constexpr int feat = SWIGLU ? kBNT / 2 : kBNT;
+  constexpr int tile_m = PAIR ? 2 * BM : BM;
+  const int nt = (prm.N + feat - 1) / feat;
+  long long tiles = ((long long)prm.rows_cap / tile_m + prm.E) * nt;  // an upper bound
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  const int units = PAIR ? num_sms() / 2 : num_sms();
+  const int n = tiles < units ? (int)tiles : units;
+  cfg.gridDim = dim3((PAIR ? 2 : 1) * n);
+  return cudaLaunchKernelEx(&cfg, kern, a, b, prm);
+}
+
+template <bool SWIGLU>
+cudaError_t fprop(const void* rows, int n_rows, const void* W, int w_rows, FpropParams prm,
+                  cudaStream_t s, const char** why) {
+  CUtensorMap a, b;
+  if (!make_map_2d(&a, rows, (uint64_t)n_rows, (uint64_t)prm.K, 64, prm.gather ? 1 : 32) ||
+      !make_map_kmajor(&b, W, (uint64_t)prm.E, (uint64_t)w_rows, (uint64_t)prm.K)) {
+    *why = "cuTensorMapEncodeTiled failed for a forward operand";
+    return cudaErrorInvalidValue;
+  }
+  // at most 128 rows in all: no expert can fill more than a one-SM tile
+  const bool pairs = prm.rows_cap > BM;
+  if (pairs) {
+    prm.part = kRowsPairs;
+    const cudaError_t e = launch_fprop<SWIGLU, true>(a, b, prm, s);
+    if (e != cudaSuccess) return e;
+  }
+  prm.part = pairs ? kRowsTails : kRowsAll;
+  prm.late_wait = pairs ? 1 : 0;
+  return launch_fprop<SWIGLU, false>(a, b, prm, s);
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu_tc(const void* x, int n_src, int src_div, const int32_t* perm,
+                             const int32_t* offsets, int rows_cap, const void* W, const void* bias,
+                             int E, int H, int I, void* Ap, void* g, void* u, void* a,
+                             uint32_t* status, cudaStream_t s, const char** why) {
+  FpropParams prm{};
+  prm.offsets = offsets;
+  prm.E = E;
+  prm.K = H;
+  prm.N = I;
+  prm.perm = perm;
+  prm.gather = perm != nullptr;
+  prm.src_div = src_div;
+  prm.n_out = perm ? n_src * src_div : rows_cap;
+  prm.bias = static_cast<const uint16_t*>(bias);
+  prm.out = static_cast<uint16_t*>(Ap);
+  prm.g = static_cast<uint16_t*>(g);
+  prm.u = static_cast<uint16_t*>(u);
+  prm.a = static_cast<uint16_t*>(a);
+  prm.status = status;
+  prm.rows_cap = rows_cap;
+  return fprop<true>(x, n_src, W, 2 * I, prm, s, why);
+}
+
+cudaError_t launch_linear_tc(const void* rows, int rows_cap, const void* W, const void* bias,
+                             const int32_t* offsets, int E, int K, int N, const void* residual,
+                             const int32_t* perm, int n_out, void* out, uint32_t* status,
+                             cudaStream_t s, const char** why) {
+  FpropParams prm{};
+  prm.offsets = offsets;
+  prm.E = E;
+  prm.K = K;
+  prm.N = N;
+  prm.perm = perm;
+  prm.src_div = 1;
+  prm.n_out = n_out;
+  prm.bias = static_cast<const uint16_t*>(bias);
+  prm.residual = static_cast<const uint16_t*>(residual);
+  prm.out = static_cast<uint16_t*>(out);
+  prm.status = status;
+  prm.rows_cap = rows_cap;
+  return fprop<false>(rows, rows_cap, W, N, prm, s, why);
+}
+
+}  // namespace lrmoe

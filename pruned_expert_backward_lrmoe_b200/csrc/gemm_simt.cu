@@ -155,7 +155,172 @@ __global__ void __launch_bounds__(NT) wgrad_simt_kernel(
   }
 }
 
+// Forward products against K-major weights: D[r][n] = sum_k A[r][k] W[e][n][k] for r in R_e.
+//   SwiGLU (swiglu != 0): a tile's 64 columns are 32 gate rows and the 32 up rows of the same
+//     features; a thread holds both of two features.  A row r = x[perm[r] / src_div].
+//   linear: out[perm[r]] = D + bias + residual[perm[r]].
+struct FpropF32 {
+  const float* rows;
+  const float* W;
+  const int32_t* offsets;
+  int E, K, N, swiglu;
+  const int32_t* perm;
+  int gather, src_div, n_out;
+  const float* bias;
+  const float* residual;
+  float* out;
+  float* g;
+  float* u;
+  float* a;
+  int rows_cap;
+  uint32_t* status;
+};
+
+__global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
+  __shared__ int tstart[kMaxExperts + 1];
+  __shared__ int scratch[33];
+  __shared__ float As[BK][BM + 4];
+  __shared__ float Bs[BK][BN + 4];
+  __shared__ int src[BM];   // source row of each tile row (-1: none)
+  __shared__ int dest[BM];  // output row of each tile row (-1: none)
+  pdl_wait();
+  pdl_trigger();
+  const int E = p.E, K = p.K, N = p.N;
+  const int feat = p.swiglu ? BN / 2 : BN;
+  const int n_tiles = (N + feat - 1) / feat;
+  const int total = offsets_invalid(p.offsets, E, p.rows_cap, p.status)
+                        ? 0 : build_dgrad_tiles(p.offsets, E, BM, n_tiles, tstart, scratch);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int lr = tid >> 2, lk = (tid & 3) * 4;  // tile row and first k of this thread's loads
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    const int e = find_group(tstart, E, t);
+    const int local = t - tstart[e];
+    const int row_beg = p.offsets[e] + (local / n_tiles) * BM;
+    const int row_end = p.offsets[e + 1];
+    const int n0 = (local % n_tiles) * feat;
+    __syncthreads();  // the last tile's epilogue has read dest
+    if (tid < BM) {
+      const int r = row_beg + tid;
+      int s = -1, d = -1;
+      if (r < row_end) {
+        s = d = r;
+        if (p.perm) {
+          d = p.perm[r];
+          if (d < 0 || d >= p.n_out) {
+            raise_status(p.status, LRMOE_ST_BAD_INDEX);
+            s = d = -1;
+          } else if (p.gather) {
+            s = d / p.src_div;
+          }
+        }
+      }
+      src[tid] = s;
+      dest[tid] = d;
+    }
+    __syncthreads();
+    // weight row behind column lr of the tile
+    int wrow = n0 + lr;
+    bool wok = wrow < N;
+    if (p.swiglu) {
+      wrow = n0 + (lr & 31);
+      wok = wrow < N;
+      wrow += lr >= 32 ? N : 0;
+    }
+    const float* wp = p.W + ((size_t)e * (p.swiglu ? 2 * N : N) + (wok ? wrow : 0)) * K;
+    const int s = src[lr];
+    const float* ap = p.rows + (size_t)(s < 0 ? 0 : s) * K;
+    float acc[4][4] = {};
+    for (int k0 = 0; k0 < K; k0 += BK) {
+      const bool kok = k0 + lk < K;  // K % 4 == 0
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 av4 = (s >= 0 && kok) ? *reinterpret_cast<const float4*>(ap + k0 + lk) : zero;
+      const float4 bv4 = (wok && kok) ? *reinterpret_cast<const float4*>(wp + k0 + lk) : zero;
+      As[lk][lr] = av4.x;
+      As[lk + 1][lr] = av4.y;
+      As[lk + 2][lr] = av4.z;
+      As[lk + 3][lr] = av4.w;
+      Bs[lk][lr] = bv4.x;
+      Bs[lk + 1][lr] = bv4.y;
+      Bs[lk + 2][lr] = bv4.z;
+      Bs[lk + 3][lr] = bv4.w;
+      __syncthreads();
+#pragma unroll
+      for (int kk = 0; kk < BK; ++kk) {
+        float av[4], bv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[i] = As[kk][ty * 4 + i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          bv[j] = Bs[kk][tx * 2 + j];
+          bv[2 + j] = Bs[kk][32 + tx * 2 + j];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = dest[ty * 4 + i];
+      if (d < 0) continue;
+      const size_t at = (size_t)d * N;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (p.swiglu) {
+          const int n = n0 + tx * 2 + j;
+          if (n >= N) continue;
+          float g = acc[i][j], u = acc[i][2 + j];
+          if (p.bias) {
+            g += p.bias[(size_t)e * 2 * N + n];
+            u += p.bias[(size_t)e * 2 * N + N + n];
+          }
+          const float a = g * sigmoidf_(g) * u;
+          if (p.g) p.g[at + n] = g;
+          if (p.u) p.u[at + n] = u;
+          if (p.a) p.a[at + n] = a;
+          p.out[(size_t)(row_beg + ty * 4 + i) * N + n] = a;
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int n = n0 + 32 * h + tx * 2 + j;
+            if (n >= N) continue;
+            float v = acc[i][2 * h + j];
+            if (p.bias) v += p.bias[(size_t)e * N + n];
+            if (p.residual) v += p.residual[at + n];
+            p.out[at + n] = v;
+          }
+        }
+      }
+    }
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_swiglu_simt(const void* x, int n_src, int src_div, const int32_t* perm,
+                               const int32_t* offsets, int rows_cap, const void* W,
+                               const void* bias, int E, int H, int I, void* Ap, void* g, void* u,
+                               void* a, uint32_t* status, cudaStream_t s) {
+  const FpropF32 p{static_cast<const float*>(x), static_cast<const float*>(W), offsets, E, H, I, 1,
+                   perm, perm != nullptr, src_div, perm ? n_src * src_div : rows_cap,
+                   static_cast<const float*>(bias), nullptr, static_cast<float*>(Ap),
+                   static_cast<float*>(g), static_cast<float*>(u), static_cast<float*>(a), rows_cap,
+                   status};
+  return launch_pdl(fprop_simt_kernel, dim3(num_sms() * 4), dim3(NT), 0, s, p);
+}
+
+cudaError_t launch_linear_simt(const void* rows, int rows_cap, const void* W, const void* bias,
+                               const int32_t* offsets, int E, int K, int N, const void* residual,
+                               const int32_t* perm, int n_out, void* out, uint32_t* status,
+                               cudaStream_t s) {
+  const FpropF32 p{static_cast<const float*>(rows), static_cast<const float*>(W), offsets, E, K, N,
+                   0, perm, 0, 1, n_out, static_cast<const float*>(bias),
+                   static_cast<const float*>(residual), static_cast<float*>(out), nullptr, nullptr,
+                   nullptr, rows_cap, status};
+  return launch_pdl(fprop_simt_kernel, dim3(num_sms() * 4), dim3(NT), 0, s, p);
+}
 
 cudaError_t launch_dgrad_simt(const void* rows, int rows_cap, const void* W,
                               const int32_t* offsets, int E, int K, int N, lrmoe_dtype dt,

@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "liblrmoe_checked.so" if os.environ.get("LRMOE_CH
 LRMOE_OK, LRMOE_ERR_INVALID_ARG, LRMOE_ERR_UNSUPPORTED, LRMOE_ERR_CUDA, LRMOE_ERR_WORKSPACE = range(5)
 LRMOE_F32, LRMOE_BF16 = 0, 1
 LRMOE_EPI_STORE, LRMOE_EPI_SWIGLU_BWD = 0, 1
+LRMOE_SCORE_SOFTMAX, LRMOE_SCORE_SIGMOID = 0, 1
 ST_BAD_EXPERT, ST_BAD_QUOTA, ST_NONFINITE, ST_TIMEOUT, ST_BAD_INDEX = 1, 2, 4, 8, 16
 
 # every symbol the header declares
@@ -32,7 +33,8 @@ EXPORTS = ("lrmoe_version", "lrmoe_status_string", "lrmoe_last_error", "lrmoe_sc
            "lrmoe_redistribute", "lrmoe_split_by_destination", "lrmoe_grouped_dgrad_wgrad",
            "lrmoe_grouped_dgrad_swiglu_gather", "lrmoe_grouped_wgrad_gather", "lrmoe_gather_rows",
            "lrmoe_group_received", "lrmoe_pack_wide", "lrmoe_split_wide",
-           "lrmoe_selftest_gemm_stall")
+           "lrmoe_selftest_gemm_stall", "lrmoe_route", "lrmoe_route_grad", "lrmoe_grouped_swiglu",
+           "lrmoe_grouped_linear", "lrmoe_grouped_bias_grad", "lrmoe_combine")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -92,6 +94,13 @@ def load() -> ctypes.CDLL:
     lib.lrmoe_gather_rows.argtypes = [P, I, I, P, I, P, P, P]
     lib.lrmoe_grouped_dgrad_wgrad.argtypes = [P, I, P, P, I, I, I, I, I, P, P, P, P, I, P, I, P, P]
     lib.lrmoe_unpack.argtypes = [P, I, P, I, I, I, I, P, P, P]
+    F = ctypes.c_float
+    lib.lrmoe_route.argtypes = [P, I, I, I, P, I, I, I, I, I, F, P, P, P, P]
+    lib.lrmoe_route_grad.argtypes = [P, I, I, I, P, I, I, I, F, P, P, P, P]
+    lib.lrmoe_grouped_swiglu.argtypes = [P, I, I, P, P, I, P, P, I, I, I, I, P, P, P, P, P, P]
+    lib.lrmoe_grouped_linear.argtypes = [P, I, P, P, P, I, I, I, I, P, P, I, P, P, P]
+    lib.lrmoe_grouped_bias_grad.argtypes = [P, I, P, I, I, I, P, I, P, P]
+    lib.lrmoe_combine.argtypes = [P, P, P, I, I, I, I, I, P, P, P, P]
     lib.lrmoe_pruned_backward.argtypes = [ctypes.POINTER(lrmoe_buffers), I, I, I, I, I, I, I, P]
     _lib = lib
     return lib
@@ -125,6 +134,23 @@ def _dt(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return LRMOE_F32
     raise ValueError(f"unsupported storage dtype {t.dtype}")
+
+
+def _fit(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, *shape: int) -> None:
+    """Refuse a tensor whose type, shape or device is not what the call will address: the C ABI
+    sees only its address.  None (an optional operand) passes."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the call is made on device "
+                         f"{torch.cuda.current_device()}")
+
+
+def _fit_status(status: Optional[torch.Tensor]) -> None:
+    if status is not None:
+        _fit("status", status, torch.int32, *((1,) if status.dim() else ()))
 
 
 # ---------------------------------------------------------------------------
@@ -330,6 +356,114 @@ def lrmoe_grouped_dgrad_wgrad(grad_rows, W, offsets, epilogue: int, out, in_rows
 def lrmoe_unpack(dXp, pos, T: int, k: int, dX, status=None, stream=None) -> None:
     _check(load().lrmoe_unpack(_ptr(dXp), dXp.shape[0], _ptr(pos), T, k, dXp.shape[-1], _dt(dXp),
                                _ptr(dX), _ptr(status), _stream(stream)))
+
+
+def lrmoe_route(logits, topk_idx, topk_w, bias=None, score_fn: int = LRMOE_SCORE_SOFTMAX,
+                n_group: int = 1, topk_group: int = 1, renormalise: bool = True,
+                scale: float = 1.0, status=None, stream=None) -> None:
+    """topk_idx, topk_w [T][k] of router logits [T][E]: softmax or sigmoid scores, an optional
+    selection bias [E], the best topk_group of n_group expert groups, renormalised weights."""
+    T, E = logits.shape
+    k = topk_idx.shape[-1]
+    _fit("logits", logits, logits.dtype, T, E)
+    _fit("topk_idx", topk_idx, torch.int32, T, k)
+    _fit("topk_w", topk_w, torch.float32, T, k)
+    _fit("bias", bias, torch.float32, E)
+    _fit_status(status)
+    _check(load().lrmoe_route(_ptr(logits), T, E, _dt(logits), _ptr(bias), k, int(score_fn),
+                              int(n_group), int(topk_group), int(bool(renormalise)), float(scale),
+                              _ptr(topk_idx), _ptr(topk_w), _ptr(status), _stream(stream)))
+
+
+def lrmoe_route_grad(logits, topk_idx, dw, dlogits, score_fn: int = LRMOE_SCORE_SOFTMAX,
+                     renormalise: bool = True, scale: float = 1.0, status=None,
+                     stream=None) -> None:
+    """dlogits [T][E] from dw (T*k values, the gradient of topk_w), for lrmoe_route's settings."""
+    T, E = logits.shape
+    k = topk_idx.shape[-1]
+    _fit("logits", logits, logits.dtype, T, E)
+    _fit("topk_idx", topk_idx, torch.int32, T, k)
+    _fit("dw", dw, torch.float32, *((T * k,) if dw.dim() == 1 else (T, k)))
+    _fit("dlogits", dlogits, logits.dtype, T, E)
+    _fit_status(status)
+    _check(load().lrmoe_route_grad(_ptr(logits), T, E, _dt(logits), _ptr(topk_idx), k,
+                                   int(score_fn), int(bool(renormalise)), float(scale), _ptr(dw),
+                                   _ptr(dlogits), _ptr(status), _stream(stream)))
+
+
+def lrmoe_grouped_swiglu(x, W_gu, offsets, Ap, perm=None, src_div: int = 1, bias=None, g=None,
+                         u=None, a=None, status=None, stream=None) -> None:
+    """Ap[r] = silu(g_r) * u_r with [g_r | u_r] = x_r . W_gu[e]^T + bias[e] for the packed rows of
+    every expert; with perm, x_r = x[perm[r] // src_div] and g, u, a are written at row perm[r]."""
+    E, I2, H = W_gu.shape
+    I, rows_cap = I2 // 2, Ap.shape[0]
+    n_out = x.shape[0] * src_div if perm is not None else rows_cap
+    _fit("W_gu", W_gu, x.dtype, E, 2 * I, H)
+    _fit("x", x, x.dtype, x.shape[0], H)
+    _fit("offsets", offsets, torch.int32, E + 1)
+    _fit("Ap", Ap, x.dtype, rows_cap, I)
+    if perm is not None:
+        _fit("perm", perm, torch.int32, perm.numel())
+        if perm.numel() < rows_cap:
+            raise ValueError(f"perm has {perm.numel()} entries for {rows_cap} packed rows")
+    _fit("bias", bias, x.dtype, E, 2 * I)
+    for name, t in (("g", g), ("u", u), ("a", a)):
+        _fit(name, t, x.dtype, n_out, I)
+    _fit_status(status)
+    _check(load().lrmoe_grouped_swiglu(_ptr(x), x.shape[0], int(src_div), _ptr(perm),
+                                       _ptr(offsets), rows_cap, _ptr(W_gu), _ptr(bias), E, H, I,
+                                       _dt(x), _ptr(Ap), _ptr(g), _ptr(u), _ptr(a), _ptr(status),
+                                       _stream(stream)))
+
+
+def lrmoe_grouped_linear(rows, W, offsets, out, bias=None, residual=None, perm=None, status=None,
+                         stream=None) -> None:
+    """out[o] = rows[r] . W[e]^T + bias[e] + residual[o], o = perm[r] (or r), for the packed rows
+    of every expert."""
+    E, N, K = W.shape
+    rows_cap, n_out = rows.shape[0], out.shape[0]
+    _fit("W", W, rows.dtype, E, N, K)
+    _fit("rows", rows, rows.dtype, rows_cap, K)
+    _fit("offsets", offsets, torch.int32, E + 1)
+    _fit("out", out, rows.dtype, n_out, N)
+    _fit("bias", bias, rows.dtype, E, N)
+    _fit("residual", residual, rows.dtype, n_out, N)
+    if perm is not None:
+        _fit("perm", perm, torch.int32, perm.numel())
+        if perm.numel() < rows_cap:
+            raise ValueError(f"perm has {perm.numel()} entries for {rows_cap} packed rows")
+    _fit_status(status)
+    _check(load().lrmoe_grouped_linear(_ptr(rows), rows_cap, _ptr(W), _ptr(bias), _ptr(offsets), E,
+                                       K, N, _dt(rows), _ptr(residual), _ptr(perm), n_out,
+                                       _ptr(out), _ptr(status), _stream(stream)))
+
+
+def lrmoe_grouped_bias_grad(grad_rows, offsets, db, accumulate: bool = False, status=None,
+                            stream=None) -> None:
+    """db[e] = the sum of expert e's packed gradient rows (fp32; added to db with accumulate)."""
+    E, N = db.shape
+    rows_cap = grad_rows.shape[0]
+    _fit("grad_rows", grad_rows, grad_rows.dtype, rows_cap, N)
+    _fit("offsets", offsets, torch.int32, E + 1)
+    _fit("db", db, torch.float32, E, N)
+    _fit_status(status)
+    _check(load().lrmoe_grouped_bias_grad(_ptr(grad_rows), rows_cap, _ptr(offsets), E, N,
+                                          _dt(grad_rows), _ptr(db), int(accumulate), _ptr(status),
+                                          _stream(stream)))
+
+
+def lrmoe_combine(y, topk_idx, topk_w, E: int, Y, residual=None, status=None, stream=None) -> None:
+    """Y[t] = the weighted sum of token t's expert outputs y [T*k][H] plus residual[t]."""
+    T, k = topk_idx.shape
+    H = Y.shape[-1]
+    _fit("y", y, y.dtype, T * k, H)
+    _fit("topk_idx", topk_idx, torch.int32, T, k)
+    _fit("topk_w", topk_w, torch.float32, T, k)
+    _fit("Y", Y, y.dtype, T, H)
+    _fit("residual", residual, y.dtype, T, H)
+    _fit_status(status)
+    _check(load().lrmoe_combine(_ptr(y), _ptr(topk_idx), _ptr(topk_w), T, k, int(E), H, _dt(y),
+                                _ptr(residual), _ptr(Y), _ptr(status), _stream(stream)))
 
 
 def lrmoe_selftest_gemm_stall(rows, W, offsets, out, two_sm: bool, limit_us: int, status,
