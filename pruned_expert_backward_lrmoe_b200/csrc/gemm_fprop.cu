@@ -37,8 +37,7 @@ struct FpropParams {
   const int32_t* offsets;
   int E, K, N;              // N: output features (SwiGLU: I)
   const int32_t* perm;      // packed row -> pair (nullptr: identity)
-  int gather;               // A rows are gathered: packed row r reads source row perm[r] / src_div
-  int src_div;
+  int src_div;              // GATHER: packed row r reads source row perm[r] / src_div
   int n_out;                // rows of the pair-order outputs
   const uint16_t* bias;     // [E][N] (SwiGLU: [E][2N]) or nullptr
   const uint16_t* residual; // linear: [n_out][N] or nullptr
@@ -127,8 +126,15 @@ __device__ __forceinline__ void add_row32(uint32_t (&r)[32], const uint16_t* v, 
   }
 }
 
-template <bool SWIGLU, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
+// Producer warps.  Packed rows need one; gathered rows come in through several, since a warp's
+// four-row loads issue one after another (about 40 ns each).
+template <bool PAIR, bool GATHER>
+constexpr int kProducers = GATHER ? (PAIR ? 8 : 4) : 1;
+template <bool PAIR, bool GATHER>
+constexpr int kFwdThreads = 32 * (kProducers<PAIR, GATHER> + 1 + kEpiWarps);
+
+template <bool SWIGLU, bool PAIR, bool GATHER>
+__global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
     const __grid_constant__ CUtensorMap tmA /* rows: 32-row boxes, or one-row boxes to gather */,
     const __grid_constant__ CUtensorMap tmB /* W [E][rows][K], 128-row boxes */,
     const FpropParams p) {
@@ -136,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
   constexpr int STAGES = L::kStages;
   constexpr int BN = kBNT;
   constexpr int kTileM = PAIR ? 2 * BM : BM;
+  constexpr int NP = kProducers<PAIR, GATHER>;
   const int E = p.E;
   uint32_t* status = p.status;
   extern __shared__ uint8_t smem_raw[];
@@ -161,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], PAIR ? 2 : 1);
+      mbar_init(&full[i], (PAIR ? 2 : 1) * NP);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -176,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
-  if (warp == 1) {
+  if (warp == NP) {
     if constexpr (PAIR) {
       tmem_alloc_pair(tmem_slot, 2 * BN);
       tmem_relinquish_pair();
@@ -202,8 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
   const uint32_t tmem_base = *tmem_slot;
   const int nk = (p.K + BK - 1) / BK;
 
-  if (warp == 0) {
-    // ---------------- producer ----------------
+  if (warp < NP) {
+    // ---------------- producers ----------------
+    // Every producer warp of both CTAs arrives on a block's barrier, also one without a group of
+    // rows to load: no block completes without it, so none can fall a ring turn behind.
     int stage = 0;
     uint32_t phase = 0;
     uint32_t armed = 0, armed_par = 0;
@@ -214,22 +223,25 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
       const int base = ti.row0 + rank * BM;  // this CTA's first row
       // Row groups of A with at least one of the expert's rows are loaded; what shared memory
       // holds in the others only reaches accumulator rows that are never stored.
-      const int unit = p.gather ? 4 : 32;
+      constexpr int unit = GATHER ? 4 : 32;
       auto groups = [&](int b) {
         int n = ti.row_end - b;
         n = n < 0 ? 0 : (n > BM ? BM : n);
         return (n + unit - 1) / unit;
       };
       const int mine = groups(base);
-      const uint32_t a_unit = (uint32_t)unit * BK * 2;
+      constexpr uint32_t a_unit = (uint32_t)unit * BK * 2;
+      // this lane's group: a producer warp has eight of the 32 four-row groups
+      const int grp = GATHER ? warp * (32 / NP) + lane : lane;
+      const bool load_a = grp < mine && (!GATHER || lane < 32 / NP);
       const uint32_t bytes =
           (uint32_t)mine * a_unit + L::kBBytes +
           (PAIR ? (uint32_t)groups(ti.row0 + BM) * a_unit + L::kBBytes : 0u);
       int src[4] = {0, 0, 0, 0};
-      if (p.gather && lane < mine) {
+      if (GATHER && load_a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = base + lane * 4 + i;
+          const int r = base + grp * 4 + i;
           const int pr = r < ti.row_end ? __ldg(p.perm + r) : 0;
           // an entry out of range reads row 0; the epilogue flags it and stores nothing
           src[i] = pr >= 0 && pr < p.n_out ? pr / p.src_div : 0;
@@ -244,17 +256,22 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
         uint8_t* sa = smem + stage * L::kStageBytes;
         uint8_t* sb = sa + L::kABytes;
         if (leader) {
-          if (lane == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+          if (lane == 0) {
+            if (warp == 0)
+              mbar_arrive_expect_tx(&full[stage], bytes);
+            else
+              mbar_arrive(&full[stage]);
+          }
           armed |= 1u << stage;
           armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           __syncwarp();
-          if (lane < mine) {
-            if (p.gather)
-              tma_gather4(sa + lane * a_unit, &tmA, &full[stage], kb * BK, src);
+          if (load_a) {
+            if constexpr (GATHER)
+              tma_gather4(sa + grp * a_unit, &tmA, &full[stage], kb * BK, src);
             else
-              tma_load_2d(sa + lane * a_unit, &tmA, &full[stage], kb * BK, base + lane * 32);
+              tma_load_2d(sa + grp * a_unit, &tmA, &full[stage], kb * BK, base + grp * 32);
           }
-          if (lane == 0) {
+          if (warp == 0 && lane == 0) {
             tma_load_3d(sb, &tmB, &full[stage], kb * BK, brow, ti.e);
             if constexpr (!PAIR)
               tma_load_3d(sb + L::kBBytes / 2, &tmB, &full[stage], kb * BK,
@@ -262,15 +279,15 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
           }
         } else {
           const uint32_t fb = lead_full + 8u * stage;
-          if (lane < mine) {
-            if (p.gather)
-              tma_gather4_pair(sa + lane * a_unit, &tmA, fb, kb * BK, src);
+          if (load_a) {
+            if constexpr (GATHER)
+              tma_gather4_pair(sa + grp * a_unit, &tmA, fb, kb * BK, src);
             else
-              tma_load_2d_pair(sa + lane * a_unit, &tmA, fb, kb * BK, base + lane * 32);
+              tma_load_2d_pair(sa + grp * a_unit, &tmA, fb, kb * BK, base + grp * 32);
           }
           __syncwarp();
           if (lane == 0) {
-            tma_load_3d_pair(sb, &tmB, fb, kb * BK, brow, ti.e);
+            if (warp == 0) tma_load_3d_pair(sb, &tmB, fb, kb * BK, brow, ti.e);
             mbar_arrive_cluster_relaxed(fb);  // the bytes are counted by the barrier itself
           }
         }
@@ -282,11 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
     }
     // every load that was started lands before shared memory is released (the leader's
     // barriers count the peer's bytes too)
-    if (leader && lane == 0)
+    if (leader && warp == 0 && lane == 0)
       for (int i = 0; i < STAGES; ++i)
         if ((armed >> i) & 1u) mbar_wait_drain<PAIR>(&full[i], (armed_par >> i) & 1u);
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == NP) {
     if (leader) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_bf16_f32(kTileM, BN, false, false);
@@ -356,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
     }
   } else {
     // ---------------- epilogue ----------------
-    const int ew = warp - 2;
+    const int ew = warp - NP - 1;
     const int q = warp & 3, half = ew >> 2;
     const int row_in_tile = rank * BM + q * 32 + lane;
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
@@ -443,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
   __syncthreads();
   if constexpr (PAIR) cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) {
+  if (warp == NP) {
     if constexpr (PAIR)
       tmem_dealloc_pair(tmem_base, 2 * BN);
     else
@@ -457,13 +474,13 @@ __global__ void __launch_bounds__(kThreads, 1) fprop_kernel(
   }
 }
 
-template <bool SWIGLU, bool PAIR>
+template <bool SWIGLU, bool PAIR, bool GATHER>
 cudaError_t launch_fprop(const CUtensorMap& a, const CUtensorMap& b, FpropParams prm,
                          cudaStream_t s) {
   using L = FwdLayout<PAIR>;
   const int smem = L::alloc(prm.E);
   if (smem > kSmemLimit) return cudaErrorInvalidConfiguration;
-  auto kern = fprop_kernel<SWIGLU, PAIR>;
+  auto kern = fprop_kernel<SWIGLU, PAIR, GATHER>;
   // set on every launch (host-side only): a cached flag would go stale when the device's
   // context is reset
   cudaError_t err =
@@ -474,7 +491,7 @@ cudaError_t launch_fprop(const CUtensorMap& a, const CUtensorMap& b, FpropParams
   const int nt = (prm.N + feat - 1) / feat;
   long long tiles = ((long long)prm.rows_cap / tile_m + prm.E) * nt;  // an upper bound
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kFwdThreads<PAIR, GATHER>);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -492,11 +509,11 @@ cudaError_t launch_fprop(const CUtensorMap& a, const CUtensorMap& b, FpropParams
   return cudaLaunchKernelEx(&cfg, kern, a, b, prm);
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool GATHER>
 cudaError_t fprop(const void* rows, int n_rows, const void* W, int w_rows, FpropParams prm,
                   cudaStream_t s, const char** why) {
   CUtensorMap a, b;
-  if (!make_map_2d(&a, rows, (uint64_t)n_rows, (uint64_t)prm.K, 64, prm.gather ? 1 : 32) ||
+  if (!make_map_2d(&a, rows, (uint64_t)n_rows, (uint64_t)prm.K, 64, GATHER ? 1 : 32) ||
       !make_map_kmajor(&b, W, (uint64_t)prm.E, (uint64_t)w_rows, (uint64_t)prm.K)) {
     *why = "cuTensorMapEncodeTiled failed for a forward operand";
     return cudaErrorInvalidValue;
@@ -505,12 +522,12 @@ cudaError_t fprop(const void* rows, int n_rows, const void* W, int w_rows, Fprop
   const bool pairs = prm.rows_cap > BM;
   if (pairs) {
     prm.part = kRowsPairs;
-    const cudaError_t e = launch_fprop<SWIGLU, true>(a, b, prm, s);
+    const cudaError_t e = launch_fprop<SWIGLU, true, GATHER>(a, b, prm, s);
     if (e != cudaSuccess) return e;
   }
   prm.part = pairs ? kRowsTails : kRowsAll;
   prm.late_wait = pairs ? 1 : 0;
-  return launch_fprop<SWIGLU, false>(a, b, prm, s);
+  return launch_fprop<SWIGLU, false, GATHER>(a, b, prm, s);
 }
 
 }  // namespace
@@ -525,7 +542,6 @@ cudaError_t launch_swiglu_tc(const void* x, int n_src, int src_div, const int32_
   prm.K = H;
   prm.N = I;
   prm.perm = perm;
-  prm.gather = perm != nullptr;
   prm.src_div = src_div;
   prm.n_out = perm ? n_src * src_div : rows_cap;
   prm.bias = static_cast<const uint16_t*>(bias);
@@ -535,7 +551,8 @@ cudaError_t launch_swiglu_tc(const void* x, int n_src, int src_div, const int32_
   prm.a = static_cast<uint16_t*>(a);
   prm.status = status;
   prm.rows_cap = rows_cap;
-  return fprop<true>(x, n_src, W, 2 * I, prm, s, why);
+  return perm ? fprop<true, true>(x, n_src, W, 2 * I, prm, s, why)
+              : fprop<true, false>(x, n_src, W, 2 * I, prm, s, why);
 }
 
 cudaError_t launch_linear_tc(const void* rows, int rows_cap, const void* W, const void* bias,
@@ -555,7 +572,7 @@ cudaError_t launch_linear_tc(const void* rows, int rows_cap, const void* W, cons
   prm.out = static_cast<uint16_t*>(out);
   prm.status = status;
   prm.rows_cap = rows_cap;
-  return fprop<false>(rows, rows_cap, W, N, prm, s, why);
+  return fprop<false, false>(rows, rows_cap, W, N, prm, s, why);
 }
 
 }  // namespace lrmoe

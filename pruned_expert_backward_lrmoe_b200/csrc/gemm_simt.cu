@@ -179,8 +179,8 @@ struct FpropF32 {
 __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
   __shared__ int tstart[kMaxExperts + 1];
   __shared__ int scratch[33];
-  __shared__ float As[BK][BM + 4];
-  __shared__ float Bs[BK][BN + 4];
+  __shared__ __align__(16) float As[BK][BM + 4];
+  __shared__ __align__(16) float Bs[BK][BN + 4];
   __shared__ int src[BM];   // source row of each tile row (-1: none)
   __shared__ int dest[BM];  // output row of each tile row (-1: none)
   pdl_wait();
@@ -230,34 +230,34 @@ __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
     const int s = src[lr];
     const float* ap = p.rows + (size_t)(s < 0 ? 0 : s) * K;
     float acc[4][4] = {};
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto load = [&](const float* at, bool ok, int k0) {  // K % 4 == 0
+      return ok && k0 + lk < K ? *reinterpret_cast<const float4*>(at + k0 + lk) : zero;
+    };
+    // the next slice's loads are in flight while this one is multiplied
+    float4 an = load(ap, s >= 0, 0), bn = load(wp, wok, 0);
     for (int k0 = 0; k0 < K; k0 += BK) {
-      const bool kok = k0 + lk < K;  // K % 4 == 0
-      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 av4 = (s >= 0 && kok) ? *reinterpret_cast<const float4*>(ap + k0 + lk) : zero;
-      const float4 bv4 = (wok && kok) ? *reinterpret_cast<const float4*>(wp + k0 + lk) : zero;
-      As[lk][lr] = av4.x;
-      As[lk + 1][lr] = av4.y;
-      As[lk + 2][lr] = av4.z;
-      As[lk + 3][lr] = av4.w;
-      Bs[lk][lr] = bv4.x;
-      Bs[lk + 1][lr] = bv4.y;
-      Bs[lk + 2][lr] = bv4.z;
-      Bs[lk + 3][lr] = bv4.w;
+      As[lk][lr] = an.x;
+      As[lk + 1][lr] = an.y;
+      As[lk + 2][lr] = an.z;
+      As[lk + 3][lr] = an.w;
+      Bs[lk][lr] = bn.x;
+      Bs[lk + 1][lr] = bn.y;
+      Bs[lk + 2][lr] = bn.z;
+      Bs[lk + 3][lr] = bn.w;
       __syncthreads();
+      an = load(ap, s >= 0, k0 + BK);
+      bn = load(wp, wok, k0 + BK);
 #pragma unroll
       for (int kk = 0; kk < BK; ++kk) {
-        float av[4], bv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) av[i] = As[kk][ty * 4 + i];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          bv[j] = Bs[kk][tx * 2 + j];
-          bv[2 + j] = Bs[kk][32 + tx * 2 + j];
-        }
+        const float4 av = *reinterpret_cast<const float4*>(&As[kk][ty * 4]);
+        const float2 b0 = *reinterpret_cast<const float2*>(&Bs[kk][tx * 2]);
+        const float2 b1 = *reinterpret_cast<const float2*>(&Bs[kk][32 + tx * 2]);
+        const float a4[4] = {av.x, av.y, av.z, av.w}, b4[4] = {b0.x, b0.y, b1.x, b1.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a4[i], b4[j], acc[i][j]);
       }
       __syncthreads();
     }

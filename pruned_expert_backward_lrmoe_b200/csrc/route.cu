@@ -43,6 +43,48 @@ __device__ __forceinline__ float load_logit(const void* z, size_t i) {
     return __ldg(static_cast<const float*>(z) + i);
 }
 
+// Logits e0 .. e0 + VPL of a row (-inf past its end).  With E a multiple of VPL every row starts
+// on a multiple of the vector (the tensor starts on 16 bytes): 16-byte loads.
+template <lrmoe_dtype DT, int VPL>
+__device__ __forceinline__ void load_row(const void* z, size_t row, int e0, int E, float (&v)[VPL]) {
+  constexpr int kBytes = VPL * (DT == LRMOE_BF16 ? 2 : 4);
+  if constexpr (kBytes >= 8) {
+    if (E % VPL == 0) {
+      constexpr int kWords = kBytes / 4;
+      uint32_t w[kWords];
+      const char* at = static_cast<const char*>(z) + (row + e0) * (DT == LRMOE_BF16 ? 2 : 4);
+      const bool ok = e0 < E;
+#pragma unroll
+      for (int i = 0; i < kWords; i += (kBytes >= 16 ? 4 : 2)) {
+        if constexpr (kBytes >= 16) {
+          const uint4 q = ok ? __ldg(reinterpret_cast<const uint4*>(at) + i / 4) : make_uint4(0, 0, 0, 0);
+          w[i] = q.x;
+          w[i + 1] = q.y;
+          w[i + 2] = q.z;
+          w[i + 3] = q.w;
+        } else {
+          const uint2 q = ok ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
+          w[i] = q.x;
+          w[i + 1] = q.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        float f;
+        if constexpr (DT == LRMOE_BF16)
+          f = bf16_bits_to_f32((i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+        else
+          f = __uint_as_float(w[i]);
+        v[i] = ok ? f : -INFINITY;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    v[i] = e0 + i < E ? load_logit<DT>(z, row + e0 + i) : -INFINITY;
+}
+
 // Order-preserving bits of a float that is not NaN; every such value maps above 0, which marks
 // an expert that cannot be chosen.
 __device__ __forceinline__ uint32_t order_bits(float f) {
@@ -148,16 +190,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
   const int E = p.E, k = p.k, G = p.groups;
   const bool plain = p.bias == nullptr && G == 1;  // the order is that of the logits
   const int e0 = lane * VPL;
+  const int n = E / G;
+  // groups of whole lanes: a lane's experts belong to one group, a group to lpg neighbouring lanes
+  const bool whole = n % VPL == 0;
+  const int lpg = whole ? n / VPL : 1, my_group = lane / lpg;
   pdl_wait();
   pdl_trigger();
   for (int t = blockIdx.x * kRouteWarps + warp; t < p.T; t += gridDim.x * kRouteWarps) {
     const size_t row = (size_t)t * E;
     float z[VPL];
+    load_row<DT, VPL>(p.logits, row, e0, E, z);
     bool bad = false;
     float zmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      z[i] = e0 + i < E ? load_logit<DT>(p.logits, row + e0 + i) : -INFINITY;
       if (isnan(z[i]) || z[i] == INFINITY) {
         bad = true;
         z[i] = -INFINITY;
@@ -165,7 +211,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       zmax = fmaxf(zmax, z[i]);
     }
     float den = 1.0f;  // softmax denominator
-    if constexpr (!SIGMOID) {
+    if (!SIGMOID && !(plain && p.renorm)) {
       zmax = warp_max(zmax);
       float sum = 0.0f;
 #pragma unroll
@@ -173,19 +219,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
         if (z[i] > -INFINITY) sum += expf(z[i] - zmax);
       den = warp_sum(sum);
     }
-    // order keys; 0 = cannot be chosen
+    // Order keys; 0 = cannot be chosen.  The scores in them are only good to the bound that the
+    // checks below allow for (fast exponential and division: 2 + 1.2 |x| ulp, under 2e-5 relative
+    // where a score is above 1e-35); the weights are computed again from the logits.
     uint32_t key[VPL];
     float smax = 0.0f;  // largest score of this lane
+    const float rden = 1.0f / den;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       bool open = z[i] > -INFINITY;
       float c = z[i];
-      if (!plain && open) {
-        const float s = SIGMOID ? sigmoid_scaled(z[i], 0.0f) : expf(z[i] - zmax) / den;
-        smax = fmaxf(smax, s);
+      if (!plain) {
+        const float s = SIGMOID ? __fdividef(1.0f, 1.0f + __expf(fminf(-z[i], 87.0f)))
+                                : __expf(z[i] - zmax) * rden;
         c = s;
+        if (open) smax = fmaxf(smax, s);
         if (p.bias) {
-          const float b = __ldg(p.bias + e0 + i);
+          const float b = e0 + i < E ? __ldg(p.bias + e0 + i) : 0.0f;
           if (isnan(b) || b == INFINITY) bad = true;
           if (!(fabsf(b) < INFINITY)) open = false;
           c = s + b;
@@ -196,23 +246,46 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
     if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
     bool sure = true;
     if (G > 1) {
-      // value of group g in lane g: the sum of the group's two largest keys
-      const int n = E / G;
-      float value = -INFINITY;
-      for (int g = 0; g < G; ++g) {
-        float a1 = -INFINITY, a2 = -INFINITY;
+      // value of each group: the sum of its two largest keys (0 bits: none)
+      float value = -INFINITY;  // of group `lane`
+      if (whole) {
+        const int pos = lane - my_group * lpg;
+        uint32_t a1 = 0u, a2 = 0u;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-          const int e = e0 + i;
-          if (key[i] != 0u && e >= g * n && e < (g + 1) * n)
-            merge_top2(a1, a2, order_value(key[i]), -INFINITY);
+          a2 = max(a2, min(a1, key[i]));
+          a1 = max(a1, key[i]);
         }
+        for (int o = 1; o < lpg; o <<= 1) {  // lane pos 0 ends with the whole group
+          const uint32_t b1 = __shfl_down_sync(kFull, a1, o), b2 = __shfl_down_sync(kFull, a2, o);
+          if (pos + o < lpg) {
+            a2 = max(max(a2, b2), min(a1, b1));
+            a1 = max(a1, b1);
+          }
+        }
+        float v = -INFINITY;
+        if (a1 != 0u) v = a2 != 0u ? order_value(a1) + order_value(a2) : order_value(a1);
+        v = __shfl_sync(kFull, v, lane < G ? lane * lpg : 0);
+        if (lane < G) value = v;
+      } else {
+        for (int g = 0; g < G; ++g) {
+          uint32_t a1 = 0u, a2 = 0u;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-          const float b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-          merge_top2(a1, a2, b1, b2);
+          for (int i = 0; i < VPL; ++i) {
+            const int e = e0 + i;
+            const uint32_t kv = e >= g * n && e < (g + 1) * n ? key[i] : 0u;
+            a2 = max(a2, min(a1, kv));
+            a1 = max(a1, kv);
+          }
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) {
+            const uint32_t b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+            a2 = max(max(a2, b2), min(a1, b1));
+            a1 = max(a1, b1);
+          }
+          if (lane == g && a1 != 0u)
+            value = a2 != 0u ? order_value(a1) + order_value(a2) : order_value(a1);
         }
-        if (lane == g && a1 > -INFINITY) value = a2 > -INFINITY ? a1 + a2 : a1;
       }
       int rank = 0;
       for (int g = 0; g < G; ++g) {
@@ -225,41 +298,41 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       const float in = -warp_max((kept >> lane) & 1u ? -value : -INFINITY);
       const float out = warp_max(open && !((kept >> lane) & 1u) ? value : -INFINITY);
       if (out > -INFINITY && kept) {
-        const float tol = 2e-5f * warp_max(smax) + 5e-7f * fmaxf(fabsf(in), fabsf(out)) + 1e-37f;
+        const float tol = 1e-4f * warp_max(smax) + 5e-7f * fmaxf(fabsf(in), fabsf(out)) + 1e-36f;
         sure = in - out > tol;
       }
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (e0 + i < E && !((kept >> ((e0 + i) / n)) & 1u)) key[i] = 0u;
-      if (p.bias == nullptr) {  // inside the kept groups the score rises with the logit
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (key[i] != 0u) key[i] = order_bits(z[i]);
+      for (int i = 0; i < VPL; ++i) {
+        if (e0 + i < E && !((kept >> (whole ? my_group : (e0 + i) / n)) & 1u)) key[i] = 0u;
+        // inside the kept groups, without bias, the score rises with the logit
+        if (p.bias == nullptr && key[i] != 0u) key[i] = order_bits(z[i]);
       }
     }
     // k rounds: the warp's largest key, its lowest holder, gone for the next round
     int mine = -1;           // expert of slot `lane`
     uint32_t mine_key = 0u;  // key of slot `lane` (lane k: the best one left)
     const int rounds = p.bias ? k + 1 : k;
-    for (int j = 0; j < rounds; ++j) {
-      uint32_t best = 0u;
+    uint32_t best = 0u;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
+    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
+    for (int j = 0; j < rounds; ++j) {
       const uint32_t top = __reduce_max_sync(kFull, best);
       if (top == 0u) break;
       const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
       int at = 0;
       if (lane == owner) {
-        bool done = false;
+        // the lowest register that holds it (scanned from the highest), then the lane's next best
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (!done && key[i] == top) {
-            done = true;
-            at = e0 + i;
-            key[i] = 0u;
-          }
+        for (int i = VPL - 1; i >= 0; --i)
+          if (key[i] == top) at = i;
+        best = 0u;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          if (i == at) key[i] = 0u;
+          best = max(best, key[i]);
+        }
       }
-      at = __shfl_sync(kFull, at, owner);
+      at = __shfl_sync(kFull, at, owner) + owner * VPL;
       if (lane == j) {
         mine = at;
         mine_key = top;
@@ -275,7 +348,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       const float s2 = __shfl_down_sync(kFull, s, 1), z2 = __shfl_down_sync(kFull, zj, 1);
       const int m2 = __shfl_down_sync(kFull, mine, 1);
       if (lane < k && mine >= 0 && lane < 31 && m2 >= 0) {
-        const float tol = 1e-5f * fmaxf(s, s2) + 2.5e-7f * fmaxf(fabsf(c), fabsf(c2)) + 1e-37f;
+        const float tol = 5e-5f * fmaxf(s, s2) + 2.5e-7f * fmaxf(fabsf(c), fabsf(c2)) + 1e-36f;
         if (c - c2 <= tol && !(zj == z2 && b == b2)) sure = false;
       }
       if (lane == 31 && k == 32) sure = false;  // its neighbour has no lane: decide in fp64
@@ -351,12 +424,39 @@ struct RouteGradParams {
   uint32_t* status;
 };
 
-template <lrmoe_dtype DT>
-__device__ __forceinline__ void store_logit(void* z, size_t i, float v) {
-  if constexpr (DT == LRMOE_BF16)
-    static_cast<unsigned short*>(z)[i] = (unsigned short)f32_to_bf16_bits_rne(v);
-  else
-    static_cast<float*>(z)[i] = v;
+template <lrmoe_dtype DT, int VPL>
+__device__ __forceinline__ void store_row(void* z, size_t row, int e0, int E, const float (&v)[VPL]) {
+  constexpr int kBytes = VPL * (DT == LRMOE_BF16 ? 2 : 4);
+  if constexpr (kBytes >= 8) {
+    if (E % VPL == 0) {  // see load_row
+      if (e0 >= E) return;
+      char* at = static_cast<char*>(z) + (row + e0) * (DT == LRMOE_BF16 ? 2 : 4);
+      uint32_t w[kBytes / 4];
+#pragma unroll
+      for (int i = 0; i < kBytes / 4; ++i) {
+        if constexpr (DT == LRMOE_BF16)
+          w[i] = f32_to_bf16_bits_rne(v[2 * i]) | (f32_to_bf16_bits_rne(v[2 * i + 1]) << 16);
+        else
+          w[i] = __float_as_uint(v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kBytes / 4; i += (kBytes >= 16 ? 4 : 2)) {
+        if constexpr (kBytes >= 16)
+          reinterpret_cast<uint4*>(at)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        else
+          *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (e0 + i >= E) continue;
+    if constexpr (DT == LRMOE_BF16)
+      static_cast<unsigned short*>(z)[row + e0 + i] = (unsigned short)f32_to_bf16_bits_rne(v[i]);
+    else
+      static_cast<float*>(z)[row + e0 + i] = v[i];
+  }
 }
 
 // Slots of one token: lane j < k holds expert, logit and d L / d (s_j or log s_j).
@@ -364,10 +464,14 @@ __device__ __forceinline__ void store_logit(void* z, size_t i, float v) {
 //   softmax:  dz_e = sum of d over the slots of e                        (renormalised)
 //             dz_e = s_e (scale sum of dw over the slots of e - scale sum_i dw_i s_i)
 //   sigmoid:  dz_e = (1 - s_e) sum over the slots of e of d_j, d_j = scale s_j dw_j if not renormalised
-template <lrmoe_dtype DT, bool SIGMOID, bool RENORM>
+// Only the third form (softmax, not renormalised) reads the whole row; the others read the
+// slots' logits and write zeros elsewhere.
+template <lrmoe_dtype DT, bool SIGMOID, bool RENORM, int VPL>
 __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p) {
+  constexpr bool DENSE = !SIGMOID && !RENORM;
   const int lane = threadIdx.x & 31;
   const int E = p.E, k = p.k;
+  const int e0 = lane * VPL;
   pdl_wait();
   pdl_trigger();
   for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 8) {
@@ -385,7 +489,8 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
     }
     const float dw = e >= 0 ? __ldg(p.dw + (size_t)t * k + lane) : 0.0f;
     float d = 0.0f;       // this slot's share of dz[e]
-    float zmax = 0.0f, inv = 0.0f, dot = 0.0f;
+    float inv = 0.0f, dot = 0.0f;
+    float v[DENSE ? VPL : 1];  // exp(z - zmax) of the lane's experts (0: not finite)
     if constexpr (RENORM) {
       const float zc = warp_max(z);
       float s = 0.0f;
@@ -398,21 +503,24 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
     } else if constexpr (SIGMOID) {
       if (e >= 0) d = p.scale * dw * sigmoid_scaled(z, 0.0f) * sigmoid_scaled(-z, 0.0f);
     } else {
+      load_row<DT, VPL>(p.logits, row, e0, E, v);
       float m = -INFINITY;
       bool bad = false;
-      for (int i = lane; i < E; i += 32) {
-        const float v = load_logit<DT>(p.logits, row + i);
-        if (isnan(v) || v == INFINITY)
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (isnan(v[i]) || v[i] == INFINITY) {
           bad = true;
-        else
-          m = fmaxf(m, v);
+          v[i] = -INFINITY;
+        }
+        m = fmaxf(m, v[i]);
       }
       if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
-      zmax = warp_max(m);
+      const float zmax = warp_max(m);
       float sum = 0.0f;
-      for (int i = lane; i < E; i += 32) {
-        const float v = load_logit<DT>(p.logits, row + i);
-        if (fabsf(v) < INFINITY) sum += expf(v - zmax);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        v[i] = v[i] > -INFINITY ? expf(v[i] - zmax) : 0.0f;
+        sum += v[i];
       }
       sum = warp_sum(sum);
       inv = sum > 0.0f ? 1.0f / sum : 0.0f;
@@ -420,22 +528,21 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
       d = p.scale * dw;
     }
     // the row: every expert's value from the slots that name it, in slot order
-    for (int i0 = 0; i0 < E; i0 += 32) {
-      const int i = i0 + lane;
-      float acc = 0.0f;
-      for (int j = 0; j < k; ++j) {
-        const int ej = __shfl_sync(kFull, e, j);
-        const float dj = __shfl_sync(kFull, d, j);
-        if (ej == i) acc += dj;
-      }
-      if (i < E) {
-        if constexpr (!RENORM && !SIGMOID) {
-          const float v = load_logit<DT>(p.logits, row + i);
-          acc = fabsf(v) < INFINITY ? (expf(v - zmax) * inv) * (acc - p.scale * dot) : 0.0f;
-        }
-        store_logit<DT>(p.dlogits, row + i, acc);
-      }
+    float acc[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const int at = __shfl_sync(kFull, e, j) - e0;
+      const float dj = __shfl_sync(kFull, d, j);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (at == i) acc[i] += dj;
     }
+    if constexpr (DENSE) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) acc[i] = v[i] * inv * (acc[i] - p.scale * dot);
+    }
+    store_row<DT, VPL>(p.dlogits, row, e0, E, acc);
   }
 }
 
@@ -460,14 +567,30 @@ cudaError_t route_by_width(const RouteParams& p, cudaStream_t s) {
   return launch_pdl(kern, dim3((unsigned)blocks), dim3(32 * kRouteWarps), smem, s, p);
 }
 
-template <lrmoe_dtype DT>
-cudaError_t route_grad_by_fn(const RouteGradParams& p, bool sigmoid, bool renorm, cudaStream_t s) {
-  auto kern = sigmoid ? (renorm ? route_grad_kernel<DT, true, true> : route_grad_kernel<DT, true, false>)
-                      : (renorm ? route_grad_kernel<DT, false, true> : route_grad_kernel<DT, false, false>);
+template <lrmoe_dtype DT, bool SIGMOID, bool RENORM>
+cudaError_t route_grad_by_width(const RouteGradParams& p, cudaStream_t s) {
+  auto kern = route_grad_kernel<DT, SIGMOID, RENORM, 32>;
+  if (p.E <= 32)
+    kern = route_grad_kernel<DT, SIGMOID, RENORM, 1>;
+  else if (p.E <= 64)
+    kern = route_grad_kernel<DT, SIGMOID, RENORM, 2>;
+  else if (p.E <= 128)
+    kern = route_grad_kernel<DT, SIGMOID, RENORM, 4>;
+  else if (p.E <= 256)
+    kern = route_grad_kernel<DT, SIGMOID, RENORM, 8>;
+  else if (p.E <= 512)
+    kern = route_grad_kernel<DT, SIGMOID, RENORM, 16>;
   long long blocks = ((long long)p.T + 7) / 8;
   const long long cap = (long long)num_sms() * 16;
   if (blocks > cap) blocks = cap;
   return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, s, p);
+}
+
+template <lrmoe_dtype DT>
+cudaError_t route_grad_by_fn(const RouteGradParams& p, bool sigmoid, bool renorm, cudaStream_t s) {
+  if (sigmoid)
+    return renorm ? route_grad_by_width<DT, true, true>(p, s) : route_grad_by_width<DT, true, false>(p, s);
+  return renorm ? route_grad_by_width<DT, false, true>(p, s) : route_grad_by_width<DT, false, false>(p, s);
 }
 
 }  // namespace

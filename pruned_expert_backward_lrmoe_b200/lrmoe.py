@@ -136,21 +136,33 @@ def _dt(t: torch.Tensor) -> int:
     raise ValueError(f"unsupported storage dtype {t.dtype}")
 
 
-def _fit(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, *shape: int) -> None:
-    """Refuse a tensor whose type, shape or device is not what the call will address: the C ABI
-    sees only its address.  None (an optional operand) passes."""
+def _arg(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, dev: int):
+    """Address of an operand (None: an optional one that is not given).  Refuses a tensor whose
+    type, shape, layout or device is not what the call will address: the C ABI sees only the
+    address."""
     if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != shape:
+        return None
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the call is made on device "
-                         f"{torch.cuda.current_device()}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor on one device with the others, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
 
 
-def _fit_status(status: Optional[torch.Tensor]) -> None:
-    if status is not None:
-        _fit("status", status, torch.int32, *((1,) if status.dim() else ()))
+def _status(t: Optional[torch.Tensor], dev: int):
+    return None if t is None else _arg("status", t, torch.int32, (1,) if t.dim() else (), dev)
+
+
+def _launch(dev: int, stream):
+    """The stream of a call whose tensors are on device `dev`, which must be the current one."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the call is made on "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
 # ---------------------------------------------------------------------------
@@ -365,14 +377,14 @@ def lrmoe_route(logits, topk_idx, topk_w, bias=None, score_fn: int = LRMOE_SCORE
     selection bias [E], the best topk_group of n_group expert groups, renormalised weights."""
     T, E = logits.shape
     k = topk_idx.shape[-1]
-    _fit("logits", logits, logits.dtype, T, E)
-    _fit("topk_idx", topk_idx, torch.int32, T, k)
-    _fit("topk_w", topk_w, torch.float32, T, k)
-    _fit("bias", bias, torch.float32, E)
-    _fit_status(status)
-    _check(load().lrmoe_route(_ptr(logits), T, E, _dt(logits), _ptr(bias), k, int(score_fn),
-                              int(n_group), int(topk_group), int(bool(renormalise)), float(scale),
-                              _ptr(topk_idx), _ptr(topk_w), _ptr(status), _stream(stream)))
+    dev = logits.get_device()
+    z = _arg("logits", logits, logits.dtype, (T, E), dev)
+    i = _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    w = _arg("topk_w", topk_w, torch.float32, (T, k), dev)
+    b = _arg("bias", bias, torch.float32, (E,), dev)
+    _check(load().lrmoe_route(z, T, E, _dt(logits), b, k, int(score_fn), int(n_group),
+                              int(topk_group), 1 if renormalise else 0, scale, i, w,
+                              _status(status, dev), _launch(dev, stream)))
 
 
 def lrmoe_route_grad(logits, topk_idx, dw, dlogits, score_fn: int = LRMOE_SCORE_SOFTMAX,
@@ -381,14 +393,20 @@ def lrmoe_route_grad(logits, topk_idx, dw, dlogits, score_fn: int = LRMOE_SCORE_
     """dlogits [T][E] from dw (T*k values, the gradient of topk_w), for lrmoe_route's settings."""
     T, E = logits.shape
     k = topk_idx.shape[-1]
-    _fit("logits", logits, logits.dtype, T, E)
-    _fit("topk_idx", topk_idx, torch.int32, T, k)
-    _fit("dw", dw, torch.float32, *((T * k,) if dw.dim() == 1 else (T, k)))
-    _fit("dlogits", dlogits, logits.dtype, T, E)
-    _fit_status(status)
-    _check(load().lrmoe_route_grad(_ptr(logits), T, E, _dt(logits), _ptr(topk_idx), k,
-                                   int(score_fn), int(bool(renormalise)), float(scale), _ptr(dw),
-                                   _ptr(dlogits), _ptr(status), _stream(stream)))
+    dev = logits.get_device()
+    z = _arg("logits", logits, logits.dtype, (T, E), dev)
+    i = _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    w = _arg("dw", dw, torch.float32, (T * k,) if dw.dim() == 1 else (T, k), dev)
+    dz = _arg("dlogits", dlogits, logits.dtype, (T, E), dev)
+    _check(load().lrmoe_route_grad(z, T, E, _dt(logits), i, k, int(score_fn),
+                                   1 if renormalise else 0, scale, w, dz, _status(status, dev),
+                                   _launch(dev, stream)))
+
+
+def _perm(perm, rows_cap: int, dev: int):
+    if perm is not None and perm.numel() < rows_cap:
+        raise ValueError(f"perm has {perm.numel()} entries for {rows_cap} packed rows")
+    return None if perm is None else _arg("perm", perm, torch.int32, (perm.numel(),), dev)
 
 
 def lrmoe_grouped_swiglu(x, W_gu, offsets, Ap, perm=None, src_div: int = 1, bias=None, g=None,
@@ -396,24 +414,19 @@ def lrmoe_grouped_swiglu(x, W_gu, offsets, Ap, perm=None, src_div: int = 1, bias
     """Ap[r] = silu(g_r) * u_r with [g_r | u_r] = x_r . W_gu[e]^T + bias[e] for the packed rows of
     every expert; with perm, x_r = x[perm[r] // src_div] and g, u, a are written at row perm[r]."""
     E, I2, H = W_gu.shape
-    I, rows_cap = I2 // 2, Ap.shape[0]
-    n_out = x.shape[0] * src_div if perm is not None else rows_cap
-    _fit("W_gu", W_gu, x.dtype, E, 2 * I, H)
-    _fit("x", x, x.dtype, x.shape[0], H)
-    _fit("offsets", offsets, torch.int32, E + 1)
-    _fit("Ap", Ap, x.dtype, rows_cap, I)
-    if perm is not None:
-        _fit("perm", perm, torch.int32, perm.numel())
-        if perm.numel() < rows_cap:
-            raise ValueError(f"perm has {perm.numel()} entries for {rows_cap} packed rows")
-    _fit("bias", bias, x.dtype, E, 2 * I)
-    for name, t in (("g", g), ("u", u), ("a", a)):
-        _fit(name, t, x.dtype, n_out, I)
-    _fit_status(status)
-    _check(load().lrmoe_grouped_swiglu(_ptr(x), x.shape[0], int(src_div), _ptr(perm),
-                                       _ptr(offsets), rows_cap, _ptr(W_gu), _ptr(bias), E, H, I,
-                                       _dt(x), _ptr(Ap), _ptr(g), _ptr(u), _ptr(a), _ptr(status),
-                                       _stream(stream)))
+    I, rows_cap, n_src, dt, dev = I2 // 2, Ap.shape[0], x.shape[0], x.dtype, x.get_device()
+    pairs = (n_src * src_div if perm is not None else rows_cap, I)
+    w = _arg("W_gu", W_gu, dt, (E, 2 * I, H), dev)
+    xp = _arg("x", x, dt, (n_src, H), dev)
+    off = _arg("offsets", offsets, torch.int32, (E + 1,), dev)
+    ap = _arg("Ap", Ap, dt, (rows_cap, I), dev)
+    pm = _perm(perm, rows_cap, dev)
+    b = _arg("bias", bias, dt, (E, 2 * I), dev)
+    gp, up, aa = (_arg("g", g, dt, pairs, dev), _arg("u", u, dt, pairs, dev),
+                  _arg("a", a, dt, pairs, dev))
+    _check(load().lrmoe_grouped_swiglu(xp, n_src, int(src_div), pm, off, rows_cap, w, b, E, H, I,
+                                       _dt(x), ap, gp, up, aa, _status(status, dev),
+                                       _launch(dev, stream)))
 
 
 def lrmoe_grouped_linear(rows, W, offsets, out, bias=None, residual=None, perm=None, status=None,
@@ -421,49 +434,42 @@ def lrmoe_grouped_linear(rows, W, offsets, out, bias=None, residual=None, perm=N
     """out[o] = rows[r] . W[e]^T + bias[e] + residual[o], o = perm[r] (or r), for the packed rows
     of every expert."""
     E, N, K = W.shape
-    rows_cap, n_out = rows.shape[0], out.shape[0]
-    _fit("W", W, rows.dtype, E, N, K)
-    _fit("rows", rows, rows.dtype, rows_cap, K)
-    _fit("offsets", offsets, torch.int32, E + 1)
-    _fit("out", out, rows.dtype, n_out, N)
-    _fit("bias", bias, rows.dtype, E, N)
-    _fit("residual", residual, rows.dtype, n_out, N)
-    if perm is not None:
-        _fit("perm", perm, torch.int32, perm.numel())
-        if perm.numel() < rows_cap:
-            raise ValueError(f"perm has {perm.numel()} entries for {rows_cap} packed rows")
-    _fit_status(status)
-    _check(load().lrmoe_grouped_linear(_ptr(rows), rows_cap, _ptr(W), _ptr(bias), _ptr(offsets), E,
-                                       K, N, _dt(rows), _ptr(residual), _ptr(perm), n_out,
-                                       _ptr(out), _ptr(status), _stream(stream)))
+    rows_cap, n_out, dt, dev = rows.shape[0], out.shape[0], rows.dtype, rows.get_device()
+    w = _arg("W", W, dt, (E, N, K), dev)
+    r = _arg("rows", rows, dt, (rows_cap, K), dev)
+    off = _arg("offsets", offsets, torch.int32, (E + 1,), dev)
+    o = _arg("out", out, dt, (n_out, N), dev)
+    b = _arg("bias", bias, dt, (E, N), dev)
+    res = _arg("residual", residual, dt, (n_out, N), dev)
+    pm = _perm(perm, rows_cap, dev)
+    _check(load().lrmoe_grouped_linear(r, rows_cap, w, b, off, E, K, N, _dt(rows), res, pm, n_out,
+                                       o, _status(status, dev), _launch(dev, stream)))
 
 
 def lrmoe_grouped_bias_grad(grad_rows, offsets, db, accumulate: bool = False, status=None,
                             stream=None) -> None:
     """db[e] = the sum of expert e's packed gradient rows (fp32; added to db with accumulate)."""
     E, N = db.shape
-    rows_cap = grad_rows.shape[0]
-    _fit("grad_rows", grad_rows, grad_rows.dtype, rows_cap, N)
-    _fit("offsets", offsets, torch.int32, E + 1)
-    _fit("db", db, torch.float32, E, N)
-    _fit_status(status)
-    _check(load().lrmoe_grouped_bias_grad(_ptr(grad_rows), rows_cap, _ptr(offsets), E, N,
-                                          _dt(grad_rows), _ptr(db), int(accumulate), _ptr(status),
-                                          _stream(stream)))
+    rows_cap, dev = grad_rows.shape[0], grad_rows.get_device()
+    r = _arg("grad_rows", grad_rows, grad_rows.dtype, (rows_cap, N), dev)
+    off = _arg("offsets", offsets, torch.int32, (E + 1,), dev)
+    out = _arg("db", db, torch.float32, (E, N), dev)
+    _check(load().lrmoe_grouped_bias_grad(r, rows_cap, off, E, N, _dt(grad_rows), out,
+                                          1 if accumulate else 0, _status(status, dev),
+                                          _launch(dev, stream)))
 
 
 def lrmoe_combine(y, topk_idx, topk_w, E: int, Y, residual=None, status=None, stream=None) -> None:
     """Y[t] = the weighted sum of token t's expert outputs y [T*k][H] plus residual[t]."""
     T, k = topk_idx.shape
-    H = Y.shape[-1]
-    _fit("y", y, y.dtype, T * k, H)
-    _fit("topk_idx", topk_idx, torch.int32, T, k)
-    _fit("topk_w", topk_w, torch.float32, T, k)
-    _fit("Y", Y, y.dtype, T, H)
-    _fit("residual", residual, y.dtype, T, H)
-    _fit_status(status)
-    _check(load().lrmoe_combine(_ptr(y), _ptr(topk_idx), _ptr(topk_w), T, k, int(E), H, _dt(y),
-                                _ptr(residual), _ptr(Y), _ptr(status), _stream(stream)))
+    H, dt, dev = Y.shape[-1], y.dtype, y.get_device()
+    yp = _arg("y", y, dt, (T * k, H), dev)
+    i = _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    w = _arg("topk_w", topk_w, torch.float32, (T, k), dev)
+    o = _arg("Y", Y, dt, (T, H), dev)
+    r = _arg("residual", residual, dt, (T, H), dev)
+    _check(load().lrmoe_combine(yp, i, w, T, k, int(E), H, _dt(y), r, o, _status(status, dev),
+                                _launch(dev, stream)))
 
 
 def lrmoe_selftest_gemm_stall(rows, W, offsets, out, two_sm: bool, limit_us: int, status,

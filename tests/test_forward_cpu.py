@@ -178,45 +178,49 @@ def test_combine_refuses(lib, at, value, code):
 def test_binding_refuses_types_and_shapes(lib):
     z = torch.zeros(4, 16)
     i, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
-    with pytest.raises(ValueError, match="topk_idx"):
-        L.lrmoe_route(z, i.long(), w)
-    with pytest.raises(ValueError, match="topk_w"):
-        L.lrmoe_route(z, i, w[:3])
-    with pytest.raises(ValueError, match="bias"):
-        L.lrmoe_route(z, i, w, bias=torch.zeros(15))
-    with pytest.raises(ValueError, match="status"):
-        L.lrmoe_route(z, i, w, status=torch.zeros(1))
-    with pytest.raises(ValueError, match="CUDA"):
-        L.lrmoe_route(z, i, w)
-    with pytest.raises(ValueError, match="dlogits"):
-        L.lrmoe_route_grad(z, i, w, z.bfloat16())
-    x, W, off = torch.zeros(4, 64), torch.zeros(3, 32, 64), torch.zeros(4, dtype=torch.int32)
-    perm = torch.zeros(8, dtype=torch.int32)
-    with pytest.raises(ValueError, match="perm has 8 entries for 9"):
-        L.lrmoe_grouped_swiglu(x, W, off, torch.zeros(9, 16), perm=perm, src_div=2)
-    with pytest.raises(ValueError, match="u: expected"):
-        L.lrmoe_grouped_swiglu(x, W, off, torch.zeros(8, 16), perm=perm, src_div=2, u=torch.zeros(4, 16))
-    with pytest.raises(ValueError, match="offsets"):
-        L.lrmoe_grouped_swiglu(x, W, off[:3], torch.zeros(8, 16), perm=perm, src_div=2)
-    with pytest.raises(ValueError, match="residual"):
-        L.lrmoe_grouped_linear(x, W, off, torch.zeros(4, 32), residual=torch.zeros(4, 64))
-    with pytest.raises(ValueError, match="W: expected"):
-        L.lrmoe_grouped_linear(x, W.bfloat16(), off, torch.zeros(4, 32))
-    with pytest.raises(ValueError, match="db"):
-        L.lrmoe_grouped_bias_grad(x, off, torch.zeros(3, 64, dtype=torch.float64))
-    with pytest.raises(ValueError, match="y: expected"):
-        L.lrmoe_combine(torch.zeros(7, 64), i, w, 8, torch.zeros(4, 64))
+
+    def refused(what, f, *args, **kw):
+        with pytest.raises(ValueError, match=what):
+            f(*args, **kw)
+
+    class Cuda(torch.Tensor):
+        """A CPU tensor that says it is on cuda:0: no call gets past the checks with it."""
+
+        def get_device(self):
+            return 0
+
+    c = lambda t: t.as_subclass(Cuda)  # noqa: E731
+    z, i, w = c(z), c(i), c(w)
+    refused("topk_idx", L.lrmoe_route, z, c(i.long()), w)
+    refused("topk_w", L.lrmoe_route, z, i, c(w[:3]))
+    refused("bias", L.lrmoe_route, z, i, w, bias=c(torch.zeros(15)))
+    refused("status", L.lrmoe_route, z, i, w, status=c(torch.zeros(1)))
+    refused("contiguous", L.lrmoe_route, c(torch.zeros(16, 4)).t(), i, w)
+    refused("CUDA tensor", L.lrmoe_route, torch.zeros(4, 16), i, w)
+    refused("CUDA tensor", L.lrmoe_route, z, i, torch.zeros(4, 2))
+    refused("dlogits", L.lrmoe_route_grad, z, i, w, c(z.bfloat16()))
+    x, W, off = c(torch.zeros(4, 64)), c(torch.zeros(3, 32, 64)), c(torch.zeros(4, dtype=torch.int32))
+    perm, new = c(torch.zeros(8, dtype=torch.int32)), lambda *s: c(torch.zeros(*s))
+    refused("perm has 8 entries for 9", L.lrmoe_grouped_swiglu, x, W, off, new(9, 16), perm=perm, src_div=2)
+    refused("perm: expected", L.lrmoe_grouped_swiglu, x, W, off, new(8, 16), perm=c(perm.long()), src_div=2)
+    refused("u: expected", L.lrmoe_grouped_swiglu, x, W, off, new(8, 16), perm=perm, src_div=2, u=new(4, 16))
+    refused("offsets", L.lrmoe_grouped_swiglu, x, W, c(off[:3]), new(8, 16), perm=perm, src_div=2)
+    refused("W_gu", L.lrmoe_grouped_swiglu, x, new(3, 33, 64), off, new(8, 16), perm=perm, src_div=2)
+    refused("residual", L.lrmoe_grouped_linear, x, W, off, new(4, 32), residual=new(4, 64))
+    refused("W: expected", L.lrmoe_grouped_linear, x, c(W.bfloat16()), off, new(4, 32))
+    refused("db", L.lrmoe_grouped_bias_grad, x, off, c(torch.zeros(3, 64, dtype=torch.float64)))
+    refused("y: expected", L.lrmoe_combine, new(7, 64), i, w, 8, new(4, 64))
 
 
 def test_binding_refuses_tensors_of_another_device(monkeypatch):
-    class Far:
-        dtype, shape, is_cuda, device = torch.float32, (4, 2), True, "cuda:1"
-
+    class Far(torch.Tensor):
         def get_device(self):
             return 1
 
+    far = torch.zeros(4, 2).as_subclass(Far)
+    with pytest.raises(ValueError, match="one device"):
+        L._arg("w", far, torch.float32, (4, 2), 0)
+    assert L._arg("w", far, torch.float32, (4, 2), 1) == far.data_ptr()
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="cuda:1"):
-        L._fit("w", Far(), torch.float32, 4, 2)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    L._fit("w", Far(), torch.float32, 4, 2)
+        L._launch(1, None)
