@@ -635,9 +635,10 @@ int lrmoe_grouped_bias_grad(const void* grad_rows, int rows_cap, const int32_t* 
   REQUIRE_PTR(grad_rows);
   REQUIRE_PTR(offsets);
   REQUIRE_PTR(db);
+  const char* why = "lrmoe_grouped_bias_grad launch";
   cudaError_t e = launch_bias_grad(grad_rows, rows_cap, offsets, E, N, dt, db, accumulate != 0,
-                                   status, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_grouped_bias_grad launch");
+                                   status, static_cast<cudaStream_t>(stream), &why);
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, why);
 }
 
 int lrmoe_combine(const void* y, const int32_t* topk_idx, const float* topk_w, int T, int k, int E,

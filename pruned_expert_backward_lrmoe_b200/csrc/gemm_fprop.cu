@@ -22,6 +22,11 @@
 // activation needs no exchange.  An expert's rows go to PAIR tiles, a last tile of at most 128
 // rows to a one-SM tile in a second launch that overlaps the first one's drain.
 //
+// Gathered rows come in by four-row TMA gathers, which the copy engine takes about 19 ns each
+// (32 a K block and CTA: more than the block's products take).  So with a long K a PAIR tile is
+// DOUBLE: 256 rows x 512 columns, both accumulators at once, half the gathers per product; else
+// the two accumulators alternate and a tile's epilogue runs under the next tile's products.
+//
 // Every tile has the same K depth, so tiles are dealt out in turn; there is no device-side
 // scheduling state that two launches or two captured graphs could share.
 //
@@ -49,14 +54,16 @@ struct FpropParams {
   int part;                 // RowPart
   int late_wait;
   int rows_cap;
+  int wide;                 // outputs' rows start on 32 bytes and N % 16 == 0
 };
 
-template <bool PAIR>
+// DOUBLE: a PAIR tile of 256 rows x 512 columns (both accumulators at once, see fprop_kernel).
+template <bool PAIR, bool DOUBLE>
 struct FwdLayout {
-  static constexpr int kStages = PAIR ? 6 : 4;
+  static constexpr int kStages = PAIR && !DOUBLE ? 6 : 4;
   static constexpr int kABytes = BM * BK * 2;                       // 16 KB
   static constexpr int kBBytes = (PAIR ? kBNT / 2 : kBNT) * BK * 2; // 16 KB / 32 KB
-  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStageBytes = kABytes + (DOUBLE ? 2 : 1) * kBBytes;
   static constexpr int kBarOff = kStages * kStageBytes;
   static constexpr int kNumBars = 2 * kStages + 5;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
@@ -71,14 +78,17 @@ struct FwdTile {
   int e, row0, row_end, n0;
 };
 
-template <bool SWIGLU, bool PAIR>
+// Output columns of an accumulator: SwiGLU features, each with its gate and up.
+template <bool SWIGLU>
+constexpr int kFeat = SWIGLU ? kBNT / 2 : kBNT;
+
+template <bool SWIGLU, bool PAIR, bool DOUBLE>
 __device__ __forceinline__ FwdTile decode_fwd(int t, const FpropParams& p, const int* offs,
                                               const int* tab, int nt) {
-  constexpr int kFeat = SWIGLU ? kBNT / 2 : kBNT;
   FwdTile ti;
   ti.e = find_group(tab, p.E, t);
   const int local = t - tab[ti.e];
-  ti.n0 = (local % nt) * kFeat;
+  ti.n0 = (local % nt) * kFeat<SWIGLU> * (DOUBLE ? 2 : 1);
   ti.row0 = dgrad_tile_row0(offs[ti.e], offs[ti.e + 1] - offs[ti.e], PAIR ? 2 * BM : BM, p.part,
                             local / nt);
   ti.row_end = offs[ti.e + 1];
@@ -107,6 +117,38 @@ __device__ __forceinline__ void tma_gather4_pair(void* dst, const void* tmap, ui
       : "memory");
 }
 
+// bf16 row segment [nb, nb + 32) of `orow`, columns >= N skipped.  wide: rows and columns lie on
+// 32 bytes, so a thread writes whole sectors.
+__device__ __forceinline__ void store_row32(const uint32_t (&r)[32], uint16_t* orow, int nb, int N,
+                                            bool wide) {
+  if (!wide) {
+    epi_store_bf16(r, orow, nb, N);
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    if (nb + v * 16 < N) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(r[16 * v + 2 * i]), __uint_as_float(r[16 * v + 2 * i + 1]));
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                       reinterpret_cast<uint64_t>(orow + nb + v * 16)),
+                   "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                   "r"(w[7])
+                   : "memory");
+    }
+  }
+}
+
+// silu(g) * u.  The exponential and the reciprocal are good to a few ulp of fp32; the result is
+// rounded to bf16.
+__device__ __forceinline__ float silu_times(float g, float u) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
+  return g * r * u;
+}
+
 // 32 values of columns [nb, nb + 32) added to r (columns >= N skipped; N % 8 == 0).  Plain
 // loads: the residual may be the output itself.
 __device__ __forceinline__ void add_row32(uint32_t (&r)[32], const uint16_t* v, int nb, int N) {
@@ -133,12 +175,13 @@ constexpr int kProducers = GATHER ? (PAIR ? 8 : 4) : 1;
 template <bool PAIR, bool GATHER>
 constexpr int kFwdThreads = 32 * (kProducers<PAIR, GATHER> + 1 + kEpiWarps);
 
-template <bool SWIGLU, bool PAIR, bool GATHER>
+template <bool SWIGLU, bool PAIR, bool GATHER, bool DOUBLE>
 __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
     const __grid_constant__ CUtensorMap tmA /* rows: 32-row boxes, or one-row boxes to gather */,
     const __grid_constant__ CUtensorMap tmB /* W [E][rows][K], 128-row boxes */,
     const FpropParams p) {
-  using L = FwdLayout<PAIR>;
+  using L = FwdLayout<PAIR, DOUBLE>;
+  constexpr int FEAT = kFeat<SWIGLU>;
   constexpr int STAGES = L::kStages;
   constexpr int BN = kBNT;
   constexpr int kTileM = PAIR ? 2 * BM : BM;
@@ -199,7 +242,8 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
     pdl_wait();
     pdl_trigger();
   }
-  const int nt = (p.N + (SWIGLU ? BN / 2 : BN) - 1) / (SWIGLU ? BN / 2 : BN);
+  constexpr int kTileN = FEAT * (DOUBLE ? 2 : 1);
+  const int nt = (p.N + kTileN - 1) / kTileN;
   int total = build_dgrad_tiles(p.offsets, E, kTileM, nt, tab, scratch, p.part);
   for (int i = threadIdx.x; i <= E; i += blockDim.x) offs_s[i] = p.offsets[i];
   tc_fence_before();
@@ -219,8 +263,9 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
     const uint32_t lead_full = PAIR ? cluster_addr(full, 0) : 0u;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
-      const FwdTile ti = decode_fwd<SWIGLU, PAIR>(t, p, offs_s, tab, nt);
+      const FwdTile ti = decode_fwd<SWIGLU, PAIR, DOUBLE>(t, p, offs_s, tab, nt);
       const int base = ti.row0 + rank * BM;  // this CTA's first row
+      const uint32_t halves = DOUBLE && ti.n0 + FEAT < p.N ? 2 : 1;
       // Row groups of A with at least one of the expert's rows are loaded; what shared memory
       // holds in the others only reaches accumulator rows that are never stored.
       constexpr int unit = GATHER ? 4 : 32;
@@ -235,8 +280,8 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
       const int grp = GATHER ? warp * (32 / NP) + lane : lane;
       const bool load_a = grp < mine && (!GATHER || lane < 32 / NP);
       const uint32_t bytes =
-          (uint32_t)mine * a_unit + L::kBBytes +
-          (PAIR ? (uint32_t)groups(ti.row0 + BM) * a_unit + L::kBBytes : 0u);
+          (uint32_t)mine * a_unit + halves * L::kBBytes +
+          (PAIR ? (uint32_t)groups(ti.row0 + BM) * a_unit + halves * L::kBBytes : 0u);
       int src[4] = {0, 0, 0, 0};
       if (GATHER && load_a) {
 #pragma unroll
@@ -273,6 +318,8 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
           }
           if (warp == 0 && lane == 0) {
             tma_load_3d(sb, &tmB, &full[stage], kb * BK, brow, ti.e);
+            if (DOUBLE && halves == 2)
+              tma_load_3d(sb + L::kBBytes, &tmB, &full[stage], kb * BK, brow + FEAT, ti.e);
             if constexpr (!PAIR)
               tma_load_3d(sb + L::kBBytes / 2, &tmB, &full[stage], kb * BK,
                           SWIGLU ? p.N + ti.n0 : ti.n0 + BN / 2, ti.e);
@@ -287,7 +334,11 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
           }
           __syncwarp();
           if (lane == 0) {
-            if (warp == 0) tma_load_3d_pair(sb, &tmB, fb, kb * BK, brow, ti.e);
+            if (warp == 0) {
+              tma_load_3d_pair(sb, &tmB, fb, kb * BK, brow, ti.e);
+              if (DOUBLE && halves == 2)
+                tma_load_3d_pair(sb + L::kBBytes, &tmB, fb, kb * BK, brow + FEAT, ti.e);
+            }
             mbar_arrive_cluster_relaxed(fb);  // the bytes are counted by the barrier itself
           }
         }
@@ -310,38 +361,90 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
       const uint32_t peer_empty = PAIR ? cluster_addr(empty, 1) : 0u;
       const uint32_t peer_tfull = PAIR ? cluster_addr(tfull, 1) : 0u;
       int stage = 0;
-      uint32_t phase = 0, acc_iter = 0;
+      uint32_t phase = 0, acc_par = 0;  // bit a: parity of accumulator a's uses so far
       bool ok = true;
-      for (int t = first; t < total && ok; t += step) {
-        const uint32_t b = acc_iter & 1u, bphase = (acc_iter >> 1) & 1u;
-        if (!__all_sync(kFull, mbar_wait_bounded(&tempty[b], bphase ^ 1u, abort_flag, status)))
-          break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + b * BN;
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!__all_sync(kFull, mbar_wait_bounded(&full[stage], phase, abort_flag, status))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t a_addr = smem_u32(smem + stage * L::kStageBytes);
-            const uint32_t b_addr = a_addr + L::kABytes;
+      // the MMAs of one K block (lane 0): A times half h of B into accumulator acc
+      auto multiply = [&](int st, int h, uint32_t acc, bool first_block) {
+        const uint32_t a_addr = smem_u32(smem + st * L::kStageBytes);
+        const uint32_t b_addr = a_addr + L::kABytes + h * L::kBBytes;
 #pragma unroll
-            for (int kk = 0; kk < BK / UK; ++kk) {
-              const uint64_t adesc = smem_desc_sw128(a_addr + kk * 32, 16, 1024);
-              const uint64_t bdesc = smem_desc_sw128(b_addr + kk * 32, 16, 1024);
-              if constexpr (PAIR)
-                tc_mma_f16_pair(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
-              else
-                tc_mma_f16(d_tmem, adesc, bdesc, idesc, (kb | kk) != 0 ? 1u : 0u);
+        for (int kk = 0; kk < BK / UK; ++kk) {
+          const uint64_t adesc = smem_desc_sw128(a_addr + kk * 32, 16, 1024);
+          const uint64_t bdesc = smem_desc_sw128(b_addr + kk * 32, 16, 1024);
+          const uint32_t more = first_block && kk == 0 ? 0u : 1u;
+          if constexpr (PAIR)
+            tc_mma_f16_pair(tmem_base + acc * BN, adesc, bdesc, idesc, more);
+          else
+            tc_mma_f16(tmem_base + acc * BN, adesc, bdesc, idesc, more);
+        }
+      };
+      auto commit = [&](uint64_t* bar, uint32_t peer_bar) {  // (lane 0) in both CTAs
+        if constexpr (PAIR) {
+          tc_commit_pair(smem_u32(bar));
+          tc_commit_pair(peer_bar);
+        } else {
+          tc_commit(bar);
+        }
+      };
+      auto wait_acc = [&](uint32_t acc) {  // drained by the epilogue
+        const bool free_ = __all_sync(kFull, mbar_wait_bounded(&tempty[acc],
+                                                               ((acc_par >> acc) & 1u) ^ 1u,
+                                                               abort_flag, status));
+        acc_par ^= 1u << acc;
+        tc_fence_after();
+        return free_;
+      };
+      auto wait_block = [&](int st, uint32_t ph) {
+        const bool there =
+            __all_sync(kFull, mbar_wait_bounded(&full[st], ph, abort_flag, status));
+        tc_fence_after();
+        return there;
+      };
+      uint32_t turn = 0;  // !DOUBLE: the tiles alternate between the accumulators
+      for (int t = first; t < total && ok; t += step) {
+        const FwdTile ti = decode_fwd<SWIGLU, PAIR, DOUBLE>(t, p, offs_s, tab, nt);
+        const bool two = DOUBLE && ti.n0 + FEAT < p.N;
+        const uint32_t acc = DOUBLE ? 0u : turn;
+        turn ^= 1u;
+        if (!(ok = wait_acc(acc))) break;
+        int kb = 0;
+        if (two) {
+          // The second accumulator is drained after the first: meanwhile multiply the first
+          // blocks into the first one, then catch up.
+          const int head = min(STAGES - 1, nk);
+          int st = stage;
+          uint32_t ph = phase;
+          for (int i = 0; i < head && ok; ++i) {
+            if (!(ok = wait_block(st, ph))) break;
+            if (lane == 0) multiply(st, 0, 0, i == 0);
+            __syncwarp();
+            if (++st == STAGES) {
+              st = 0;
+              ph ^= 1u;
             }
-            if constexpr (PAIR) {
-              tc_commit_pair(smem_u32(&empty[stage]));
-              tc_commit_pair(peer_empty + 8u * stage);
-            } else {
-              tc_commit(&empty[stage]);
+          }
+          if (!ok || !(ok = wait_acc(1))) break;
+          for (; kb < head; ++kb) {
+            if (lane == 0) {
+              multiply(stage, 1, 1, kb == 0);
+              commit(&empty[stage], peer_empty + 8u * stage);
             }
+            __syncwarp();
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        for (; kb < nk; ++kb) {
+          if (!(ok = wait_block(stage, phase))) break;
+          if (lane == 0) {
+            multiply(stage, 0, acc, kb == 0);
+            if (two) {
+              if (kb + 1 == nk) commit(&tfull[0], peer_tfull);
+              multiply(stage, 1, 1, false);
+            }
+            commit(&empty[stage], peer_empty + 8u * stage);
           }
           __syncwarp();
           if (++stage == STAGES) {
@@ -351,15 +454,10 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
         }
         if (!ok) break;
         if (lane == 0) {
-          if constexpr (PAIR) {
-            tc_commit_pair(smem_u32(&tfull[b]));
-            tc_commit_pair(peer_tfull + 8u * b);
-          } else {
-            tc_commit(&tfull[b]);
-          }
+          if (!two || nk < STAGES) commit(&tfull[acc], peer_tfull + 8u * acc);
+          if (two) commit(&tfull[1], peer_tfull + 8u);
         }
         __syncwarp();
-        ++acc_iter;
       }
       // every issued MMA has finished before tensor memory is released
       if (lane == 0) {
@@ -378,7 +476,8 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
     const int row_in_tile = rank * BM + q * 32 + lane;
     const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
     const uint32_t lead_tempty = PAIR ? cluster_addr(tempty, 0) : 0u;
-    uint32_t acc_iter = 0;
+    const bool wide = p.wide != 0;
+    uint32_t acc_par = 0, turn = 0;  // acc_par: bit a is the parity of accumulator a's uses
     auto release_acc = [&](uint32_t b) {
       tc_fence_before();
       __syncwarp();
@@ -390,7 +489,7 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
       }
     };
     for (int t = first; t < total; t += step) {
-      const FwdTile ti = decode_fwd<SWIGLU, PAIR>(t, p, offs_s, tab, nt);
+      const FwdTile ti = decode_fwd<SWIGLU, PAIR, DOUBLE>(t, p, offs_s, tab, nt);
       const int row = ti.row0 + row_in_tile;
       bool row_ok = row < ti.row_end;
       int orow = row;
@@ -401,59 +500,65 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
           row_ok = false;
         }
       }
-      const uint32_t b = acc_iter & 1u, bphase = (acc_iter >> 1) & 1u;
-      if (!__all_sync(kFull, mbar_wait_bounded(&tfull[b], bphase, abort_flag, status))) break;
-      tc_fence_after();
-      if constexpr (SWIGLU) {
-        const uint16_t* bias = p.bias ? p.bias + (size_t)ti.e * 2 * p.N : nullptr;
+      const int halves = DOUBLE && ti.n0 + FEAT < p.N ? 2 : 1;
+      bool ok = true;
+      for (int h = 0; h < halves; ++h) {
+        const uint32_t b = DOUBLE ? (uint32_t)h : turn;
+        ok = __all_sync(kFull, mbar_wait_bounded(&tfull[b], (acc_par >> b) & 1u, abort_flag, status));
+        acc_par ^= 1u << b;
+        if (!ok) break;
+        tc_fence_after();
+        const int c0 = ti.n0 + h * FEAT;  // first column of this accumulator
+        if constexpr (SWIGLU) {
+          const uint16_t* bias = p.bias ? p.bias + (size_t)ti.e * 2 * p.N : nullptr;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int f = half * 64 + c * 32;  // feature inside the tile
-          const int nb = ti.n0 + f;
-          uint32_t rg[32], ru[32];
-          tmem_ld_32x32b_x32(lane_base + b * BN + f, rg);
-          tmem_ld_32x32b_x32(lane_base + b * BN + BN / 2 + f, ru);
-          tmem_wait_ld();
-          reg_fence(rg);
-          reg_fence(ru);
-          if (c == 1) release_acc(b);
-          if (row_ok && nb < p.N) {
-            if (bias) {
-              add_row32(rg, bias, nb, p.N);
-              add_row32(ru, bias + p.N, nb, p.N);
-            }
-            const size_t at = (size_t)orow * p.N;
-            if (p.g) epi_store_bf16(rg, p.g + at, nb, p.N);
-            if (p.u) epi_store_bf16(ru, p.u + at, nb, p.N);
+          for (int c = 0; c < 2; ++c) {
+            const int f = half * 64 + c * 32;  // feature inside the accumulator
+            const int nb = c0 + f;
+            uint32_t rg[32], ru[32];
+            tmem_ld_32x32b_x32(lane_base + b * BN + f, rg);
+            tmem_ld_32x32b_x32(lane_base + b * BN + BN / 2 + f, ru);
+            tmem_wait_ld();
+            reg_fence(rg);
+            reg_fence(ru);
+            if (c == 1) release_acc(b);
+            if (row_ok && nb < p.N) {
+              if (bias) {
+                add_row32(rg, bias, nb, p.N);
+                add_row32(ru, bias + p.N, nb, p.N);
+              }
+              const size_t at = (size_t)orow * p.N;
+              if (p.g) store_row32(rg, p.g + at, nb, p.N, wide);
+              if (p.u) store_row32(ru, p.u + at, nb, p.N, wide);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float g = __uint_as_float(rg[i]);
-              rg[i] = __float_as_uint(g * sigmoid_fast(g) * __uint_as_float(ru[i]));
+              for (int i = 0; i < 32; ++i)
+                rg[i] = __float_as_uint(silu_times(__uint_as_float(rg[i]), __uint_as_float(ru[i])));
+              if (p.a) store_row32(rg, p.a + at, nb, p.N, wide);
+              store_row32(rg, p.out + (size_t)row * p.N, nb, p.N, wide);
             }
-            if (p.a) epi_store_bf16(rg, p.a + at, nb, p.N);
-            epi_store_bf16(rg, p.out + (size_t)row * p.N, nb, p.N);
           }
-        }
-      } else {
-        const uint16_t* bias = p.bias ? p.bias + (size_t)ti.e * p.N : nullptr;
+        } else {
+          const uint16_t* bias = p.bias ? p.bias + (size_t)ti.e * p.N : nullptr;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = half * 128 + c * 32;
-          const int nb = ti.n0 + col;
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(lane_base + b * BN + col, r);
-          tmem_wait_ld();
-          reg_fence(r);
-          if (c == 3) release_acc(b);
-          if (row_ok && nb < p.N) {
-            const size_t at = (size_t)orow * p.N;
-            if (bias) add_row32(r, bias, nb, p.N);
-            if (p.residual) add_row32(r, p.residual + at, nb, p.N);
-            epi_store_bf16(r, p.out + at, nb, p.N);
+          for (int c = 0; c < 4; ++c) {
+            const int col = half * 128 + c * 32;
+            const int nb = c0 + col;
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(lane_base + b * BN + col, r);
+            tmem_wait_ld();
+            reg_fence(r);
+            if (c == 3) release_acc(b);
+            if (row_ok && nb < p.N) {
+              const size_t at = (size_t)orow * p.N;
+              if (bias) add_row32(r, bias, nb, p.N);
+              if (p.residual) add_row32(r, p.residual + at, nb, p.N);
+              store_row32(r, p.out + at, nb, p.N, wide);
+            }
           }
         }
       }
-      ++acc_iter;
+      if (!ok) break;
+      turn ^= 1u;
     }
   }
   tc_fence_before();
@@ -474,19 +579,19 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
   }
 }
 
-template <bool SWIGLU, bool PAIR, bool GATHER>
+template <bool SWIGLU, bool PAIR, bool GATHER, bool DOUBLE>
 cudaError_t launch_fprop(const CUtensorMap& a, const CUtensorMap& b, FpropParams prm,
                          cudaStream_t s) {
-  using L = FwdLayout<PAIR>;
+  using L = FwdLayout<PAIR, DOUBLE>;
   const int smem = L::alloc(prm.E);
   if (smem > kSmemLimit) return cudaErrorInvalidConfiguration;
-  auto kern = fprop_kernel<SWIGLU, PAIR, GATHER>;
+  auto kern = fprop_kernel<SWIGLU, PAIR, GATHER, DOUBLE>;
   // set on every launch (host-side only): a cached flag would go stale when the device's
   // context is reset
   cudaError_t err =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (err != cudaSuccess) return err;
-  constexpr int feat = SWIGLU ? kBNT / 2 : kBNT;
+  constexpr int feat = kFeat<SWIGLU> * (DOUBLE ? 2 : 1);
   constexpr int tile_m = PAIR ? 2 * BM : BM;
   const int nt = (prm.N + feat - 1) / feat;
   long long tiles = ((long long)prm.rows_cap / tile_m + prm.E) * nt;  // an upper bound
@@ -518,16 +623,29 @@ cudaError_t fprop(const void* rows, int n_rows, const void* W, int w_rows, Fprop
     *why = "cuTensorMapEncodeTiled failed for a forward operand";
     return cudaErrorInvalidValue;
   }
+  auto on32 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 31u) == 0; };
+  prm.wide = prm.N % 16 == 0 && on32(prm.out) && on32(prm.g) && on32(prm.u) && on32(prm.a);
   // at most 128 rows in all: no expert can fill more than a one-SM tile
   const bool pairs = prm.rows_cap > BM;
   if (pairs) {
     prm.part = kRowsPairs;
-    const cudaError_t e = launch_fprop<SWIGLU, true, GATHER>(a, b, prm, s);
+    cudaError_t e;
+    if constexpr (GATHER) {
+      // DOUBLE halves the gathered rows per flop, but a tile's epilogue is not overlapped by the
+      // next tile's products: worth it over long K.  T = 16384, H = 4096, I = 1408: 2.86 ms
+      // against 3.07; H = 2048, I = 768, T = 8192: 0.58 against 0.60.  (Packed rows: 2.70 against
+      // 2.53, so they keep the single tile.)
+      const bool twice = prm.K >= 2048 && prm.N > kFeat<SWIGLU>;
+      e = twice ? launch_fprop<SWIGLU, true, true, true>(a, b, prm, s)
+                : launch_fprop<SWIGLU, true, true, false>(a, b, prm, s);
+    } else {
+      e = launch_fprop<SWIGLU, true, false, false>(a, b, prm, s);
+    }
     if (e != cudaSuccess) return e;
   }
   prm.part = pairs ? kRowsTails : kRowsAll;
   prm.late_wait = pairs ? 1 : 0;
-  return launch_fprop<SWIGLU, false, GATHER>(a, b, prm, s);
+  return launch_fprop<SWIGLU, false, GATHER, false>(a, b, prm, s);
 }
 
 }  // namespace

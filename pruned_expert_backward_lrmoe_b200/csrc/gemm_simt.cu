@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(NT) wgrad_simt_kernel(
 }
 
 // Forward products against K-major weights: D[r][n] = sum_k A[r][k] W[e][n][k] for r in R_e.
-//   SwiGLU (swiglu != 0): a tile's 64 columns are 32 gate rows and the 32 up rows of the same
-//     features; a thread holds both of two features.  A row r = x[perm[r] / src_div].
+//   SwiGLU (swiglu != 0): half of a tile's columns are gate rows, half the up rows of the same
+//     features, and a thread holds both of a feature.  A row r = x[perm[r] / src_div].
 //   linear: out[perm[r]] = D + bias + residual[perm[r]].
 struct FpropF32 {
   const float* rows;
@@ -176,17 +176,24 @@ struct FpropF32 {
   uint32_t* status;
 };
 
+// Ring of FS 16-deep K slices, copied asynchronously as they lie in memory; rows of 20 floats keep
+// the 16-byte reads of neighbouring columns in different banks.
+constexpr int FS = 4, FP = BK + 4;
+
+// TN: tile columns.  64, or 32 where 64-column tiles would leave SMs without one.
+template <int TN>
 __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
+  constexpr int CJ = TN / 16;  // columns of a thread
   __shared__ int tstart[kMaxExperts + 1];
   __shared__ int scratch[33];
-  __shared__ __align__(16) float As[BK][BM + 4];
-  __shared__ __align__(16) float Bs[BK][BN + 4];
+  __shared__ __align__(16) float As[FS][BM][FP];
+  __shared__ __align__(16) float Bs[FS][TN][FP];
   __shared__ int src[BM];   // source row of each tile row (-1: none)
   __shared__ int dest[BM];  // output row of each tile row (-1: none)
   pdl_wait();
   pdl_trigger();
   const int E = p.E, K = p.K, N = p.N;
-  const int feat = p.swiglu ? BN / 2 : BN;
+  const int feat = p.swiglu ? TN / 2 : TN;
   const int n_tiles = (N + feat - 1) / feat;
   const int total = offsets_invalid(p.offsets, E, p.rows_cap, p.status)
                         ? 0 : build_dgrad_tiles(p.offsets, E, BM, n_tiles, tstart, scratch);
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
     const int row_beg = p.offsets[e] + (local / n_tiles) * BM;
     const int row_end = p.offsets[e + 1];
     const int n0 = (local % n_tiles) * feat;
-    __syncthreads();  // the last tile's epilogue has read dest
+    __syncthreads();  // the last tile's slices and dest have been read
     if (tid < BM) {
       const int r = row_beg + tid;
       int s = -1, d = -1;
@@ -220,58 +227,74 @@ __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
     __syncthreads();
     // weight row behind column lr of the tile
     int wrow = n0 + lr;
-    bool wok = wrow < N;
+    bool wok = lr < TN && wrow < N;
     if (p.swiglu) {
-      wrow = n0 + (lr & 31);
-      wok = wrow < N;
-      wrow += lr >= 32 ? N : 0;
+      wrow = n0 + lr % (TN / 2);
+      wok = lr < TN && wrow < N;
+      wrow += lr >= TN / 2 ? N : 0;
     }
     const float* wp = p.W + ((size_t)e * (p.swiglu ? 2 * N : N) + (wok ? wrow : 0)) * K;
     const int s = src[lr];
     const float* ap = p.rows + (size_t)(s < 0 ? 0 : s) * K;
-    float acc[4][4] = {};
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto load = [&](const float* at, bool ok, int k0) {  // K % 4 == 0
-      return ok && k0 + lk < K ? *reinterpret_cast<const float4*>(at + k0 + lk) : zero;
+    float acc[4][CJ] = {};
+    const int steps = (K + BK - 1) / BK;
+    auto fetch = [&](int step) {  // this thread's 16 bytes of A and B (K % 4 == 0), or zeros
+      const int k0 = step * BK;
+      const bool ok = k0 + lk < K;
+      const int f = step % FS;
+      if (step < steps) {
+        cp_async_16(&As[f][lr][lk], s >= 0 && ok ? ap + k0 + lk : p.rows, s >= 0 && ok ? 16 : 0);
+        if (lr < TN)
+          cp_async_16(&Bs[f][lr][lk], wok && ok ? wp + k0 + lk : p.W, wok && ok ? 16 : 0);
+      }
+      cp_async_commit();
     };
-    // the next slice's loads are in flight while this one is multiplied
-    float4 an = load(ap, s >= 0, 0), bn = load(wp, wok, 0);
-    for (int k0 = 0; k0 < K; k0 += BK) {
-      As[lk][lr] = an.x;
-      As[lk + 1][lr] = an.y;
-      As[lk + 2][lr] = an.z;
-      As[lk + 3][lr] = an.w;
-      Bs[lk][lr] = bn.x;
-      Bs[lk + 1][lr] = bn.y;
-      Bs[lk + 2][lr] = bn.z;
-      Bs[lk + 3][lr] = bn.w;
-      __syncthreads();
-      an = load(ap, s >= 0, k0 + BK);
-      bn = load(wp, wok, k0 + BK);
 #pragma unroll
-      for (int kk = 0; kk < BK; ++kk) {
-        const float4 av = *reinterpret_cast<const float4*>(&As[kk][ty * 4]);
-        const float2 b0 = *reinterpret_cast<const float2*>(&Bs[kk][tx * 2]);
-        const float2 b1 = *reinterpret_cast<const float2*>(&Bs[kk][32 + tx * 2]);
-        const float a4[4] = {av.x, av.y, av.z, av.w}, b4[4] = {b0.x, b0.y, b1.x, b1.y};
+    for (int i = 0; i < FS - 1; ++i) fetch(i);
+    for (int step = 0; step < steps; ++step) {
+      cp_async_wait_group<FS - 2>();
+      __syncthreads();  // slice `step` is there for every thread, slice step - 1 is read
+      fetch(step + FS - 1);
+      const int f = step % FS;
+#pragma unroll
+      for (int kk = 0; kk < BK; kk += 4) {
+        float4 av[4], bv[CJ];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[i] = *reinterpret_cast<const float4*>(&As[f][ty + 16 * i][kk]);
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) bv[j] = *reinterpret_cast<const float4*>(&Bs[f][tx + 16 * j][kk]);
+        // one k at a time over all of the thread's outputs: independent multiply-adds
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a4[i], b4[j], acc[i][j]);
+          for (int j = 0; j < CJ; ++j) acc[i][j] = fmaf(av[i].x, bv[j].x, acc[i][j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < CJ; ++j) acc[i][j] = fmaf(av[i].y, bv[j].y, acc[i][j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < CJ; ++j) acc[i][j] = fmaf(av[i].z, bv[j].z, acc[i][j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < CJ; ++j) acc[i][j] = fmaf(av[i].w, bv[j].w, acc[i][j]);
       }
-      __syncthreads();
     }
+    // columns tx + 16 j of the tile: SwiGLU holds gate features tx (and tx + 16) and their ups
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int d = dest[ty * 4 + i];
+      const int m = ty + 16 * i;
+      const int d = dest[m];
       if (d < 0) continue;
       const size_t at = (size_t)d * N;
+      if (p.swiglu) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (p.swiglu) {
-          const int n = n0 + tx * 2 + j;
+        for (int j = 0; j < CJ / 2; ++j) {
+          const int n = n0 + tx + 16 * j;
           if (n >= N) continue;
-          float g = acc[i][j], u = acc[i][2 + j];
+          float g = acc[i][j], u = acc[i][CJ / 2 + j];
           if (p.bias) {
             g += p.bias[(size_t)e * 2 * N + n];
             u += p.bias[(size_t)e * 2 * N + N + n];
@@ -280,21 +303,29 @@ __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
           if (p.g) p.g[at + n] = g;
           if (p.u) p.u[at + n] = u;
           if (p.a) p.a[at + n] = a;
-          p.out[(size_t)(row_beg + ty * 4 + i) * N + n] = a;
-        } else {
+          p.out[(size_t)(row_beg + m) * N + n] = a;
+        }
+      } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int n = n0 + 32 * h + tx * 2 + j;
-            if (n >= N) continue;
-            float v = acc[i][2 * h + j];
-            if (p.bias) v += p.bias[(size_t)e * N + n];
-            if (p.residual) v += p.residual[at + n];
-            p.out[at + n] = v;
-          }
+        for (int j = 0; j < CJ; ++j) {
+          const int n = n0 + tx + 16 * j;
+          if (n >= N) continue;
+          float v = acc[i][j];
+          if (p.bias) v += p.bias[(size_t)e * N + n];
+          if (p.residual) v += p.residual[at + n];
+          p.out[at + n] = v;
         }
       }
     }
   }
+}
+
+cudaError_t fprop_simt(const FpropF32& p, cudaStream_t s) {
+  const int feat = p.swiglu ? 32 : 64;
+  // an upper bound of the 64-column tiles; under two per SM the narrow ones spread better
+  const long long tiles = ((long long)p.rows_cap / BM + p.E) * ((p.N + feat - 1) / feat);
+  auto kern = tiles < 2ll * num_sms() ? fprop_simt_kernel<32> : fprop_simt_kernel<64>;
+  return launch_pdl(kern, dim3(num_sms() * 4), dim3(NT), 0, s, p);
 }
 
 }  // namespace
@@ -308,7 +339,7 @@ cudaError_t launch_swiglu_simt(const void* x, int n_src, int src_div, const int3
                    static_cast<const float*>(bias), nullptr, static_cast<float*>(Ap),
                    static_cast<float*>(g), static_cast<float*>(u), static_cast<float*>(a), rows_cap,
                    status};
-  return launch_pdl(fprop_simt_kernel, dim3(num_sms() * 4), dim3(NT), 0, s, p);
+  return fprop_simt(p, s);
 }
 
 cudaError_t launch_linear_simt(const void* rows, int rows_cap, const void* W, const void* bias,
@@ -319,7 +350,7 @@ cudaError_t launch_linear_simt(const void* rows, int rows_cap, const void* W, co
                    0, perm, 0, 1, n_out, static_cast<const float*>(bias),
                    static_cast<const float*>(residual), static_cast<float*>(out), nullptr, nullptr,
                    nullptr, rows_cap, status};
-  return launch_pdl(fprop_simt_kernel, dim3(num_sms() * 4), dim3(NT), 0, s, p);
+  return fprop_simt(p, s);
 }
 
 cudaError_t launch_dgrad_simt(const void* rows, int rows_cap, const void* W,

@@ -85,21 +85,27 @@ __device__ __forceinline__ void load_row(const void* z, size_t row, int e0, int 
     v[i] = e0 + i < E ? load_logit<DT>(z, row + e0 + i) : -INFINITY;
 }
 
-// Order-preserving bits of a float that is not NaN; every such value maps above 0, which marks
-// an expert that cannot be chosen.
+// Order-preserving bits of a float that is not NaN (-0 orders as +0).  -inf marks an expert that
+// cannot be chosen; its bits lie below those of every other value.
 __device__ __forceinline__ uint32_t order_bits(float f) {
-  const uint32_t b = __float_as_uint(f + 0.0f);  // -0 orders as +0
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const int b = __float_as_int(f + 0.0f);
+  return (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
 }
+constexpr uint32_t kShut = 0x007fffffu;  // order_bits(-inf)
 
 __device__ __forceinline__ float order_value(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
+  return order_value(__reduce_max_sync(kFull, order_bits(v)));
+}
+
+// 1/x to one ulp, for keys that are checked against an error bound (see route_kernel)
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 template <typename F>
@@ -183,9 +189,94 @@ __device__ __noinline__ int topk_fp64(double* key, int E, int k, int lane) {
   return mine;
 }
 
+// The k experts of the largest keys in slot order, by threshold: at least k + 1 of the warp's keys
+// reach the (k + 1)-th largest of the 32 lane maxima, and few more do (11 or so of 128 for
+// k = 8).  Those that do are brought to one per lane and ranked by counting (key, lower
+// expert first).  Lane j gets slot j (mine, mine_key), lane k the best one left.  False (nothing
+// set) where more than 32 reach the threshold.
+template <int VPL>
+__device__ __forceinline__ bool topk_by_threshold(const uint32_t (&key)[VPL], int k, int lane,
+                                                  uint64_t* box, int& mine, uint32_t& mine_key) {
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
+  uint32_t bar = 0u;
+  if (VPL > 1) {  // the largest maxima one after another, equal ones together
+    uint32_t left = best;
+    for (int seen = 0; seen <= k;) {
+      bar = __reduce_max_sync(kFull, left);
+      if (bar <= kShut) break;
+      const bool top = left == bar;
+      seen += __popc(__ballot_sync(kFull, top));
+      if (top) left = 0u;
+    }
+  }
+  if (bar <= kShut) bar = kShut + 1u;  // fewer lanes than that hold a key: take all keys
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const bool in = key[i] >= bar;
+    const unsigned who = __ballot_sync(kFull, in);
+    const int at = count + __popc(who & ((1u << lane) - 1u));
+    if (in && at < 32) box[at] = ((uint64_t)key[i] << 32) | (uint32_t)~(lane * VPL + i);
+    count += __popc(who);
+  }
+  if (count > 32) return false;
+  __syncwarp();
+  const uint64_t own = lane < count ? box[lane] : 0ull;
+  if (lane >= count) box[lane] = 0ull;
+  __syncwarp();
+  int rank = 0;
+  for (int c = 0; c < count; c += 4) {  // all lanes read one address: a broadcast
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(box + c);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(box + c + 2);
+    rank += (a.x > own ? 1 : 0) + (a.y > own ? 1 : 0) + (b.x > own ? 1 : 0) + (b.y > own ? 1 : 0);
+  }
+  __syncwarp();
+  if (lane < count) box[rank] = own;
+  __syncwarp();
+  if (lane < count && lane <= k) {
+    const uint64_t got = box[lane];
+    mine = (int)~(uint32_t)got;
+    mine_key = (uint32_t)(got >> 32);
+  }
+  __syncwarp();  // before the next token's keys
+  return true;
+}
+
+// The same in k + 1 rounds: the warp's largest key, its lowest holder, gone for the next round.
+template <int VPL>
+__device__ __noinline__ void topk_by_rounds(uint32_t (&key)[VPL], int k, int lane, int& mine,
+                                            uint32_t& mine_key) {
+  for (int j = 0; j < (k < 31 ? k + 1 : 32); ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
+    const uint32_t top = __reduce_max_sync(kFull, best);
+    if (top <= kShut) break;
+    const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
+    int at = 0;
+    if (lane == owner) {
+      // the lowest register that holds it (scanned from the highest)
+#pragma unroll
+      for (int i = VPL - 1; i >= 0; --i)
+        if (key[i] == top) at = i;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i == at) key[i] = kShut;
+    }
+    at = __shfl_sync(kFull, at, owner) + owner * VPL;
+    if (lane == j) {
+      mine = at;
+      mine_key = top;
+    }
+  }
+}
+
 template <lrmoe_dtype DT, bool SIGMOID, int VPL>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 : 1) route_kernel(const RouteParams p) {
   extern __shared__ double keys64[];  // [kRouteWarps][E], when a bias or groups are given
+  __shared__ __align__(16) uint64_t boxes[kRouteWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = p.E, k = p.k, G = p.groups;
   const bool plain = p.bias == nullptr && G == 1;  // the order is that of the logits
@@ -196,61 +287,76 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
   const int lpg = whole ? n / VPL : 1, my_group = lane / lpg;
   pdl_wait();
   pdl_trigger();
+  // this lane's biases; one that is not finite shuts its expert
+  float bias[VPL];
+  bool bad_bias = false;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    bias[i] = p.bias != nullptr && e0 + i < E ? __ldg(p.bias + e0 + i) : 0.0f;
+    if (!(bias[i] < INFINITY)) {
+      bad_bias = true;
+      bias[i] = -INFINITY;
+    }
+  }
   for (int t = blockIdx.x * kRouteWarps + warp; t < p.T; t += gridDim.x * kRouteWarps) {
     const size_t row = (size_t)t * E;
     float z[VPL];
     load_row<DT, VPL>(p.logits, row, e0, E, z);
-    bool bad = false;
+    bool bad = bad_bias;
     float zmax = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      if (isnan(z[i]) || z[i] == INFINITY) {
+      if (!(z[i] < INFINITY)) {  // NaN or +inf
         bad = true;
         z[i] = -INFINITY;
       }
       zmax = fmaxf(zmax, z[i]);
     }
-    float den = 1.0f;  // softmax denominator
-    if (!SIGMOID && !(plain && p.renorm)) {
-      zmax = warp_max(zmax);
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (z[i] > -INFINITY) sum += expf(z[i] - zmax);
-      den = warp_sum(sum);
-    }
-    // Order keys; 0 = cannot be chosen.  The scores in them are only good to the bound that the
-    // checks below allow for (fast exponential and division: 2 + 1.2 |x| ulp, under 2e-5 relative
-    // where a score is above 1e-35); the weights are computed again from the logits.
+    if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
+    if (!SIGMOID && !(plain && p.renorm)) zmax = warp_max(zmax);
+    // Order keys, with a bound on the error of their scores.  sigmoid: an exponential (2 ulp),
+    // an addition, a reciprocal (1 ulp): 4.2e-7 s.  softmax: the difference z - zmax
+    // rounds by 6e-8 |z - zmax|, the exponential by 2 ulp, the reciprocal and the product by 2; the
+    // denominator (37 additions, 2.3e-6) is the same for all keys of the token:
+    // (3.2e-6 + 6e-8 |z - zmax|) s.  Scores under 2e-38 count as 2e-38 or 0.
     uint32_t key[VPL];
     float smax = 0.0f;  // largest score of this lane
-    const float rden = 1.0f / den;
+    if (plain) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      bool open = z[i] > -INFINITY;
-      float c = z[i];
-      if (!plain) {
-        const float s = SIGMOID ? __fdividef(1.0f, 1.0f + __expf(fminf(-z[i], 87.0f)))
-                                : __expf(z[i] - zmax) * rden;
-        c = s;
-        if (open) smax = fmaxf(smax, s);
-        if (p.bias) {
-          const float b = e0 + i < E ? __ldg(p.bias + e0 + i) : 0.0f;
-          if (isnan(b) || b == INFINITY) bad = true;
-          if (!(fabsf(b) < INFINITY)) open = false;
-          c = s + b;
+      for (int i = 0; i < VPL; ++i) key[i] = order_bits(z[i]);
+    } else {
+      float sc[VPL];
+      float rden = 1.0f;
+      if constexpr (SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sc[i] = fast_rcp(1.0f + expf(fminf(-z[i], 87.0f)));
+      } else {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          sc[i] = z[i] > -INFINITY ? expf(z[i] - zmax) : 0.0f;
+          sum += sc[i];
         }
+        rden = fast_rcp(warp_sum(sum));
       }
-      key[i] = open ? order_bits(c) : 0u;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const float s = SIGMOID ? sc[i] : sc[i] * rden;
+        smax = fmaxf(smax, z[i] > -INFINITY ? s : 0.0f);
+        key[i] = order_bits(z[i] > -INFINITY ? s + bias[i] : -INFINITY);
+      }
     }
-    if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
     bool sure = true;
     if (G > 1) {
-      // value of each group: the sum of its two largest keys (0 bits: none)
+      // value of each group: the sum of its two largest keys
       float value = -INFINITY;  // of group `lane`
+      auto value_of = [](uint32_t a1, uint32_t a2) {
+        const float v = order_value(a1);  // -inf: no expert left in the group
+        return a2 > kShut ? v + order_value(a2) : v;
+      };
       if (whole) {
         const int pos = lane - my_group * lpg;
-        uint32_t a1 = 0u, a2 = 0u;
+        uint32_t a1 = kShut, a2 = kShut;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
           a2 = max(a2, min(a1, key[i]));
@@ -263,17 +369,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
             a1 = max(a1, b1);
           }
         }
-        float v = -INFINITY;
-        if (a1 != 0u) v = a2 != 0u ? order_value(a1) + order_value(a2) : order_value(a1);
-        v = __shfl_sync(kFull, v, lane < G ? lane * lpg : 0);
+        const float v = __shfl_sync(kFull, value_of(a1, a2), lane < G ? lane * lpg : 0);
         if (lane < G) value = v;
       } else {
         for (int g = 0; g < G; ++g) {
-          uint32_t a1 = 0u, a2 = 0u;
+          uint32_t a1 = kShut, a2 = kShut;
 #pragma unroll
           for (int i = 0; i < VPL; ++i) {
             const int e = e0 + i;
-            const uint32_t kv = e >= g * n && e < (g + 1) * n ? key[i] : 0u;
+            const uint32_t kv = e >= g * n && e < (g + 1) * n ? key[i] : kShut;
             a2 = max(a2, min(a1, kv));
             a1 = max(a1, kv);
           }
@@ -283,8 +387,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
             a2 = max(max(a2, b2), min(a1, b1));
             a1 = max(a1, b1);
           }
-          if (lane == g && a1 != 0u)
-            value = a2 != 0u ? order_value(a1) + order_value(a2) : order_value(a1);
+          if (lane == g) value = value_of(a1, a2);
         }
       }
       int rank = 0;
@@ -298,48 +401,24 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       const float in = -warp_max((kept >> lane) & 1u ? -value : -INFINITY);
       const float out = warp_max(open && !((kept >> lane) & 1u) ? value : -INFINITY);
       if (out > -INFINITY && kept) {
-        const float tol = 1e-4f * warp_max(smax) + 5e-7f * fmaxf(fabsf(in), fabsf(out)) + 1e-36f;
+        // four scores are compared (|z - zmax| s is below 0.4 smax e^-1 ...: 1e-5 covers it)
+        const float tol = (SIGMOID ? 2e-6f : 1.5e-5f) * warp_max(smax) +
+                          5e-7f * fmaxf(fabsf(in), fabsf(out)) + 1e-36f;
         sure = in - out > tol;
       }
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (e0 + i < E && !((kept >> (whole ? my_group : (e0 + i) / n)) & 1u)) key[i] = 0u;
+        if (e0 + i < E && !((kept >> (whole ? my_group : (e0 + i) / n)) & 1u)) key[i] = kShut;
         // inside the kept groups, without bias, the score rises with the logit
-        if (p.bias == nullptr && key[i] != 0u) key[i] = order_bits(z[i]);
+        if (p.bias == nullptr && key[i] != kShut) key[i] = order_bits(z[i]);
       }
     }
-    // k rounds: the warp's largest key, its lowest holder, gone for the next round
-    int mine = -1;           // expert of slot `lane`
-    uint32_t mine_key = 0u;  // key of slot `lane` (lane k: the best one left)
-    const int rounds = p.bias ? k + 1 : k;
-    uint32_t best = 0u;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
-    for (int j = 0; j < rounds; ++j) {
-      const uint32_t top = __reduce_max_sync(kFull, best);
-      if (top == 0u) break;
-      const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
-      int at = 0;
-      if (lane == owner) {
-        // the lowest register that holds it (scanned from the highest), then the lane's next best
-#pragma unroll
-        for (int i = VPL - 1; i >= 0; --i)
-          if (key[i] == top) at = i;
-        best = 0u;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          if (i == at) key[i] = 0u;
-          best = max(best, key[i]);
-        }
-      }
-      at = __shfl_sync(kFull, at, owner) + owner * VPL;
-      if (lane == j) {
-        mine = at;
-        mine_key = top;
-      }
-    }
+    int mine = -1;             // expert of slot `lane`
+    uint32_t mine_key = kShut; // its key (lane k: the best one left)
+    if (k == 32 || !topk_by_threshold<VPL>(key, k, lane, boxes[warp], mine, mine_key))
+      topk_by_rounds<VPL>(key, k, lane, mine, mine_key);
     float zj = mine >= 0 ? load_logit<DT>(p.logits, row + mine) : -INFINITY;
-    if (p.bias) {
+    if (p.bias != nullptr) {
       // neighbours of the order that fp32 cannot tell apart
       const float c = mine >= 0 ? order_value(mine_key) : 0.0f;
       const float b = mine >= 0 ? __ldg(p.bias + mine) : 0.0f;
@@ -348,7 +427,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       const float s2 = __shfl_down_sync(kFull, s, 1), z2 = __shfl_down_sync(kFull, zj, 1);
       const int m2 = __shfl_down_sync(kFull, mine, 1);
       if (lane < k && mine >= 0 && lane < 31 && m2 >= 0) {
-        const float tol = 5e-5f * fmaxf(s, s2) + 2.5e-7f * fmaxf(fabsf(c), fabsf(c2)) + 1e-36f;
+        const float rel = SIGMOID ? 1e-6f : 7e-6f + 1.3e-7f * (zmax - fminf(zj, z2));
+        const float tol = rel * fmaxf(s, s2) + 2.5e-7f * fmaxf(fabsf(c), fabsf(c2)) + 1e-36f;
         if (c - c2 <= tol && !(zj == z2 && b == b2)) sure = false;
       }
       if (lane == 31 && k == 32) sure = false;  // its neighbour has no lane: decide in fp64
@@ -368,8 +448,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       for (int i = 0; i < VPL; ++i) {
         if (e0 + i >= E) continue;
         double c = -INFINITY;
-        const float b = p.bias ? __ldg(p.bias + e0 + i) : 0.0f;
-        if (z[i] > -INFINITY && fabsf(b) < INFINITY) {
+        const float b = bias[i];
+        if (z[i] > -INFINITY && b > -INFINITY) {
           c = SIGMOID ? 1.0 / (1.0 + exp(-(double)z[i]))
                       : exp((double)z[i] - (double)zmax) / den64;
           c += (double)b;
@@ -401,8 +481,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
       if (mine >= 0) s = SIGMOID ? sigmoid_scaled(zj, fminf(zc, 0.0f)) : expf(zj - zc);
       const float sum = warp_sum(s);
       if (mine >= 0) s = s / sum;
-    } else if (mine >= 0) {
-      s = SIGMOID ? sigmoid_scaled(zj, 0.0f) : expf(zj - zmax) / den;
+    } else if constexpr (SIGMOID) {
+      if (mine >= 0) s = sigmoid_scaled(zj, 0.0f);
+    } else {
+      float den = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) den += z[i] > -INFINITY ? expf(z[i] - zmax) : 0.0f;
+      den = warp_sum(den);
+      if (mine >= 0) s = expf(zj - zmax) / den;
     }
     if (slot) {
       p.idx[(size_t)t * k + lane] = mine;
@@ -459,24 +545,42 @@ __device__ __forceinline__ void store_row(void* z, size_t row, int e0, int E, co
   }
 }
 
-// Slots of one token: lane j < k holds expert, logit and d L / d (s_j or log s_j).
-//   renormalised: p_j = s_j / S,  d_j = scale p_j (dw_j - sum_i p_i dw_i)       (= s_j dL/ds_j)
-//   softmax:  dz_e = sum of d over the slots of e                        (renormalised)
-//             dz_e = s_e (scale sum of dw over the slots of e - scale sum_i dw_i s_i)
-//   sigmoid:  dz_e = (1 - s_e) sum over the slots of e of d_j, d_j = scale s_j dw_j if not renormalised
-// Only the third form (softmax, not renormalised) reads the whole row; the others read the
-// slots' logits and write zeros elsewhere.
-template <lrmoe_dtype DT, bool SIGMOID, bool RENORM, int VPL>
-__global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p) {
-  constexpr bool DENSE = !SIGMOID && !RENORM;
-  const int lane = threadIdx.x & 31;
+// One token's slots, slot j in lane j of the token's SUB lanes:
+//   renormalised: p_j = s_j / S, d_j = scale p_j (dw_j - sum_i p_i dw_i), for sigmoid times (1 - s_j)
+//   sigmoid:      d_j = scale dw_j s_j (1 - s_j)
+// and dz_e = sum of d over the slots of e: the row is zeros but for the slots' experts, so only
+// their logits are read.  SUB lanes take a token (k <= SUB), a warp 32 / SUB neighbouring tokens.
+template <lrmoe_dtype DT, bool SIGMOID, bool RENORM, int SUB>
+__global__ void __launch_bounds__(256) route_grad_sparse_kernel(const RouteGradParams p) {
+  constexpr int kTokens = 32 / SUB;
+  constexpr int kSize = DT == LRMOE_BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 31, sub = lane / SUB, j = lane % SUB;
   const int E = p.E, k = p.k;
-  const int e0 = lane * VPL;
+  auto sum = [](float v) {
+#pragma unroll
+    for (int o = SUB / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+  };
+  const long long step = (long long)gridDim.x * 8 * kTokens;
   pdl_wait();
   pdl_trigger();
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 8) {
+  for (long long t0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kTokens; t0 < p.T; t0 += step) {
+    const long long t = t0 + sub;
+    const bool live = t < p.T;
     const size_t row = (size_t)t * E;
-    int e = lane < k ? __ldg(p.idx + (size_t)t * k + lane) : -1;
+    int e = live && j < k ? __ldg(p.idx + t * k + j) : -1;
+    if (live) {  // zeros first; the slots' values follow
+      char* at = static_cast<char*>(p.dlogits) + row * kSize;
+      const int bytes = E * kSize;
+      if (bytes % 16 == 0) {
+        for (int i = j * 16; i < bytes; i += SUB * 16)
+          *reinterpret_cast<uint4*>(at + i) = make_uint4(0, 0, 0, 0);
+      } else if (bytes % 4 == 0) {
+        for (int i = j * 4; i < bytes; i += SUB * 4) *reinterpret_cast<uint32_t*>(at + i) = 0u;
+      } else {
+        for (int i = j * 2; i < bytes; i += SUB * 2) *reinterpret_cast<unsigned short*>(at + i) = 0;
+      }
+    }
     if (e >= E) {
       raise_status(p.status, LRMOE_ST_BAD_EXPERT);
       e = -1;
@@ -487,61 +591,102 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
       e = -1;
       z = -INFINITY;
     }
-    const float dw = e >= 0 ? __ldg(p.dw + (size_t)t * k + lane) : 0.0f;
-    float d = 0.0f;       // this slot's share of dz[e]
-    float inv = 0.0f, dot = 0.0f;
-    float v[DENSE ? VPL : 1];  // exp(z - zmax) of the lane's experts (0: not finite)
+    const float dw = e >= 0 ? __ldg(p.dw + t * k + j) : 0.0f;
+    float d = 0.0f;
     if constexpr (RENORM) {
-      const float zc = warp_max(z);
+      float zc = z;
+#pragma unroll
+      for (int o = SUB / 2; o >= 1; o >>= 1) zc = fmaxf(zc, __shfl_xor_sync(kFull, zc, o));
       float s = 0.0f;
       if (e >= 0) s = SIGMOID ? sigmoid_scaled(z, fminf(zc, 0.0f)) : expf(z - zc);
-      const float sum = warp_sum(s);
-      const float pj = e >= 0 ? s / sum : 0.0f;
-      const float mean = warp_sum(pj * dw);
+      const float total = sum(s);
+      const float pj = e >= 0 ? s / total : 0.0f;
+      const float mean = sum(pj * dw);
       d = p.scale * pj * (dw - mean);
       if (SIGMOID && e >= 0) d *= sigmoid_scaled(-z, 0.0f);
-    } else if constexpr (SIGMOID) {
-      if (e >= 0) d = p.scale * dw * sigmoid_scaled(z, 0.0f) * sigmoid_scaled(-z, 0.0f);
     } else {
-      load_row<DT, VPL>(p.logits, row, e0, E, v);
-      float m = -INFINITY;
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (isnan(v[i]) || v[i] == INFINITY) {
-          bad = true;
-          v[i] = -INFINITY;
-        }
-        m = fmaxf(m, v[i]);
-      }
-      if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
-      const float zmax = warp_max(m);
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        v[i] = v[i] > -INFINITY ? expf(v[i] - zmax) : 0.0f;
-        sum += v[i];
-      }
-      sum = warp_sum(sum);
-      inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-      dot = warp_sum(e >= 0 ? dw * (expf(z - zmax) * inv) : 0.0f);
-      d = p.scale * dw;
+      if (e >= 0) d = p.scale * dw * sigmoid_scaled(z, 0.0f) * sigmoid_scaled(-z, 0.0f);
     }
-    // the row: every expert's value from the slots that name it, in slot order
+    // An expert named by several slots: the first of them adds the others, in slot order.  Lanes
+    // without a slot have a number of their own.
+    const unsigned same = __match_any_sync(kFull, e >= 0 ? (sub << 16) | e : ~lane);
+    bool write = e >= 0;
+    if (__any_sync(kFull, (same & (same - 1u)) != 0u)) {
+      const float own = d;
+      d = 0.0f;
+      for (int i = 0; i < 32; ++i) {
+        const float di = __shfl_sync(kFull, own, i);
+        if ((same >> i) & 1u) d += di;
+      }
+      write = write && lane == __ffs(same) - 1;
+    }
+    __syncwarp();  // the zeros are written before the values
+    if (write) {
+      if constexpr (DT == LRMOE_BF16)
+        static_cast<unsigned short*>(p.dlogits)[row + e] = (unsigned short)f32_to_bf16_bits_rne(d);
+      else
+        static_cast<float*>(p.dlogits)[row + e] = d;
+    }
+  }
+}
+
+// Softmax, not renormalised: every logit gets a gradient,
+//   dz_e = s_e (scale sum of dw over the slots of e - scale sum_i dw_i s_i).
+template <lrmoe_dtype DT, int VPL>
+__global__ void __launch_bounds__(256) route_grad_dense_kernel(const RouteGradParams p) {
+  const int lane = threadIdx.x & 31;
+  const int E = p.E, k = p.k;
+  const int e0 = lane * VPL;
+  pdl_wait();
+  pdl_trigger();
+  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 8) {
+    const size_t row = (size_t)t * E;
+    float v[VPL];  // then exp(z - zmax) of the lane's experts (0: not finite)
+    load_row<DT, VPL>(p.logits, row, e0, E, v);
+    int e = lane < k ? __ldg(p.idx + (size_t)t * k + lane) : -1;
+    if (e >= E) {
+      raise_status(p.status, LRMOE_ST_BAD_EXPERT);
+      e = -1;
+    }
+    const float z = e >= 0 ? load_logit<DT>(p.logits, row + e) : -INFINITY;
+    if (!(fabsf(z) < INFINITY)) e = -1;  // NaN and +inf are flagged with the row
+    const float dw = e >= 0 ? __ldg(p.dw + (size_t)t * k + lane) : 0.0f;
+    float m = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (!(v[i] < INFINITY)) {
+        bad = true;
+        v[i] = -INFINITY;
+      }
+      m = fmaxf(m, v[i]);
+    }
+    if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
+    const float zmax = warp_max(m);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      v[i] = v[i] > -INFINITY ? expf(v[i] - zmax) : 0.0f;
+      sum += v[i];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float dot = warp_sum(e >= 0 ? dw * (expf(z - zmax) * inv) : 0.0f);
     float acc[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const int at = __shfl_sync(kFull, e, j) - e0;
-      const float dj = __shfl_sync(kFull, d, j);
+    for (int i = 0; i < VPL; ++i) acc[i] = -dot;
+    for (int j0 = 0; j0 < k; j0 += 8) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (at == i) acc[i] += dj;
-    }
-    if constexpr (DENSE) {
+      for (int j = 0; j < 8; ++j) {  // lanes past k hold no expert
+        const int at = __shfl_sync(kFull, e, j0 + j) - e0;
+        const float dj = __shfl_sync(kFull, dw, j0 + j);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] = v[i] * inv * (acc[i] - p.scale * dot);
+        for (int i = 0; i < VPL; ++i)
+          if (at == i) acc[i] += dj;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] = v[i] * inv * (p.scale * acc[i]);
     store_row<DT, VPL>(p.dlogits, row, e0, E, acc);
   }
 }
@@ -562,24 +707,43 @@ cudaError_t route_by_width(const RouteParams& p, cudaStream_t s) {
   const bool plain = p.bias == nullptr && p.groups == 1;
   const size_t smem = plain ? 0 : sizeof(double) * (size_t)kRouteWarps * p.E;  // <= 32 KB
   long long blocks = ((long long)p.T + kRouteWarps - 1) / kRouteWarps;
-  const long long cap = (long long)num_sms() * 32;
+  // about what is resident at once: a warp keeps its biases over several tokens
+  const long long cap = (long long)num_sms() * (p.E <= 256 ? 8 : 4);
   if (blocks > cap) blocks = cap;
   return launch_pdl(kern, dim3((unsigned)blocks), dim3(32 * kRouteWarps), smem, s, p);
 }
 
 template <lrmoe_dtype DT, bool SIGMOID, bool RENORM>
-cudaError_t route_grad_by_width(const RouteGradParams& p, cudaStream_t s) {
-  auto kern = route_grad_kernel<DT, SIGMOID, RENORM, 32>;
+cudaError_t route_grad_sparse(const RouteGradParams& p, cudaStream_t s) {
+  auto kern = route_grad_sparse_kernel<DT, SIGMOID, RENORM, 32>;
+  int sub = 32;
+  if (p.k <= 8) {
+    kern = route_grad_sparse_kernel<DT, SIGMOID, RENORM, 8>;
+    sub = 8;
+  } else if (p.k <= 16) {
+    kern = route_grad_sparse_kernel<DT, SIGMOID, RENORM, 16>;
+    sub = 16;
+  }
+  const long long tokens = 8 * (32 / sub);  // of a block
+  long long blocks = (p.T + tokens - 1) / tokens;
+  const long long cap = (long long)num_sms() * 32;
+  if (blocks > cap) blocks = cap;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(256), 0, s, p);
+}
+
+template <lrmoe_dtype DT>
+cudaError_t route_grad_dense(const RouteGradParams& p, cudaStream_t s) {
+  auto kern = route_grad_dense_kernel<DT, 32>;
   if (p.E <= 32)
-    kern = route_grad_kernel<DT, SIGMOID, RENORM, 1>;
+    kern = route_grad_dense_kernel<DT, 1>;
   else if (p.E <= 64)
-    kern = route_grad_kernel<DT, SIGMOID, RENORM, 2>;
+    kern = route_grad_dense_kernel<DT, 2>;
   else if (p.E <= 128)
-    kern = route_grad_kernel<DT, SIGMOID, RENORM, 4>;
+    kern = route_grad_dense_kernel<DT, 4>;
   else if (p.E <= 256)
-    kern = route_grad_kernel<DT, SIGMOID, RENORM, 8>;
+    kern = route_grad_dense_kernel<DT, 8>;
   else if (p.E <= 512)
-    kern = route_grad_kernel<DT, SIGMOID, RENORM, 16>;
+    kern = route_grad_dense_kernel<DT, 16>;
   long long blocks = ((long long)p.T + 7) / 8;
   const long long cap = (long long)num_sms() * 16;
   if (blocks > cap) blocks = cap;
@@ -588,9 +752,8 @@ cudaError_t route_grad_by_width(const RouteGradParams& p, cudaStream_t s) {
 
 template <lrmoe_dtype DT>
 cudaError_t route_grad_by_fn(const RouteGradParams& p, bool sigmoid, bool renorm, cudaStream_t s) {
-  if (sigmoid)
-    return renorm ? route_grad_by_width<DT, true, true>(p, s) : route_grad_by_width<DT, true, false>(p, s);
-  return renorm ? route_grad_by_width<DT, false, true>(p, s) : route_grad_by_width<DT, false, false>(p, s);
+  if (!renorm) return sigmoid ? route_grad_sparse<DT, true, false>(p, s) : route_grad_dense<DT>(p, s);
+  return sigmoid ? route_grad_sparse<DT, true, true>(p, s) : route_grad_sparse<DT, false, true>(p, s);
 }
 
 }  // namespace

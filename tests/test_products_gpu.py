@@ -139,6 +139,13 @@ def test_swiglu_gathered(sizes, H, I, k, bias, outputs, dt):
         assert (np64(t)[rest] == SENTINEL).all()
 
 
+@pytest.mark.parametrize("I", [128, 136, 264, 392])
+@pytest.mark.parametrize("H", [2048, 2056, 4104])
+def test_swiglu_gathered_long_rows(H, I):
+    """Long K (wide tiles): one, two and three column blocks."""
+    test_swiglu_gathered("edges", H, I, 4, True, "gua", "bf16")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_swiglu_packed_rows_equal_gathered_ones(dt):
     sz, H, I, k = SIZES["edges"], 136, 72, 4
