@@ -29,6 +29,8 @@ struct RouteParams {
   const void* logits;
   const float* bias;
   int T, E, k, groups, keep_groups, renorm;
+  int n;    // experts of a group
+  int lpg;  // lanes of a group, if a group is whole lanes of the kernel's width, else 0
   float scale;
   int32_t* idx;
   float* w;
@@ -281,10 +283,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
   const int E = p.E, k = p.k, G = p.groups;
   const bool plain = p.bias == nullptr && G == 1;  // the order is that of the logits
   const int e0 = lane * VPL;
-  const int n = E / G;
+  const int n = p.n;
   // groups of whole lanes: a lane's experts belong to one group, a group to lpg neighbouring lanes
-  const bool whole = n % VPL == 0;
-  const int lpg = whole ? n / VPL : 1, my_group = lane / lpg;
+  const bool whole = p.lpg > 0;
+  const int lpg = p.lpg, my_group = G > 1 && whole ? lane / lpg : 0;
   pdl_wait();
   pdl_trigger();
   // this lane's biases; one that is not finite shuts its expert
@@ -298,7 +300,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       bias[i] = -INFINITY;
     }
   }
-  for (int t = blockIdx.x * kRouteWarps + warp; t < p.T; t += gridDim.x * kRouteWarps) {
+  // 64-bit: T may be near 2^31
+  for (long long t = (long long)blockIdx.x * kRouteWarps + warp; t < p.T;
+       t += (long long)gridDim.x * kRouteWarps) {
     const size_t row = (size_t)t * E;
     float z[VPL];
     load_row<DT, VPL>(p.logits, row, e0, E, z);
@@ -310,49 +314,46 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
         bad = true;
         z[i] = -INFINITY;
       }
-      zmax = fmaxf(zmax, z[i]);
+      if (!SIGMOID) zmax = fmaxf(zmax, z[i]);
     }
     if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
     if (!SIGMOID && !(plain && p.renorm)) zmax = warp_max(zmax);
-    // Order keys, with a bound on the error of their scores.  sigmoid: an exponential (2 ulp),
-    // an addition, a reciprocal (1 ulp): 4.2e-7 s.  softmax: the difference z - zmax
-    // rounds by 6e-8 |z - zmax|, the exponential by 2 ulp, the reciprocal and the product by 2; the
-    // denominator (37 additions, 2.3e-6) is the same for all keys of the token:
-    // (3.2e-6 + 6e-8 |z - zmax|) s.  Scores under 2e-38 count as 2e-38 or 0.
+    // Order keys, with a bound on the error of their scores (u = 6e-8).  The fast exponential is
+    // off by (4 + |x|) u relative, the reciprocal by 2 u.  sigmoid: (8 + |z|) u s.  softmax: the
+    // difference z - zmax rounds by |z - zmax| u, and the denominator (37 additions) is the same
+    // for all keys of the token: (50 + 2 |z - zmax|) u s.  Scores under 2e-38 count as that or 0.
     uint32_t key[VPL];
-    float smax = 0.0f;  // largest score of this lane
+    float rden = 1.0f;  // softmax: the largest score
     if (plain) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = order_bits(z[i]);
     } else {
       float sc[VPL];
-      float rden = 1.0f;
       if constexpr (SIGMOID) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) sc[i] = fast_rcp(1.0f + expf(fminf(-z[i], 87.0f)));
+        for (int i = 0; i < VPL; ++i) sc[i] = fast_rcp(1.0f + __expf(fminf(-z[i], 87.0f)));
       } else {
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-          sc[i] = z[i] > -INFINITY ? expf(z[i] - zmax) : 0.0f;
+          sc[i] = z[i] > -INFINITY ? __expf(z[i] - zmax) : 0.0f;
           sum += sc[i];
         }
         rden = fast_rcp(warp_sum(sum));
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sc[i] *= rden;
       }
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const float s = SIGMOID ? sc[i] : sc[i] * rden;
-        smax = fmaxf(smax, z[i] > -INFINITY ? s : 0.0f);
-        key[i] = order_bits(z[i] > -INFINITY ? s + bias[i] : -INFINITY);
-      }
+      for (int i = 0; i < VPL; ++i)
+        key[i] = order_bits(z[i] > -INFINITY ? sc[i] + bias[i] : -INFINITY);
     }
     bool sure = true;
     if (G > 1) {
-      // value of each group: the sum of its two largest keys
-      float value = -INFINITY;  // of group `lane`
+      // value of each group, as order bits in lane g: the sum of the group's two largest keys
+      uint32_t value = 0u;
       auto value_of = [](uint32_t a1, uint32_t a2) {
         const float v = order_value(a1);  // -inf: no expert left in the group
-        return a2 > kShut ? v + order_value(a2) : v;
+        return order_bits(a2 > kShut ? v + order_value(a2) : v);
       };
       if (whole) {
         const int pos = lane - my_group * lpg;
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
             a1 = max(a1, b1);
           }
         }
-        const float v = __shfl_sync(kFull, value_of(a1, a2), lane < G ? lane * lpg : 0);
+        const uint32_t v = __shfl_sync(kFull, value_of(a1, a2), lane < G ? lane * lpg : 0);
         if (lane < G) value = v;
       } else {
         for (int g = 0; g < G; ++g) {
@@ -390,27 +391,40 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
           if (lane == g) value = value_of(a1, a2);
         }
       }
-      int rank = 0;
-      for (int g = 0; g < G; ++g) {
-        const float v = __shfl_sync(kFull, value, g);
-        rank += (v > value || (v == value && g < lane)) ? 1 : 0;
+      // the best ones, the lower of equal ones first
+      unsigned kept = 0u;
+      uint32_t last = 0u;
+      for (int j = 0; j < p.keep_groups; ++j) {
+        const uint32_t top = __reduce_max_sync(kFull, value);
+        if (top <= kShut) break;
+        const unsigned who = __ballot_sync(kFull, value == top);
+        const int g = __ffs(who) - 1;
+        kept |= 1u << g;
+        last = top;
+        if (lane == g) value = 0u;
       }
-      const bool open = lane < G && value > -INFINITY;
-      const unsigned kept = __ballot_sync(kFull, open && rank < p.keep_groups);
-      // the last kept value against the first that is not kept
-      const float in = -warp_max((kept >> lane) & 1u ? -value : -INFINITY);
-      const float out = warp_max(open && !((kept >> lane) & 1u) ? value : -INFINITY);
-      if (out > -INFINITY && kept) {
-        // four scores are compared (|z - zmax| s is below 0.4 smax e^-1 ...: 1e-5 covers it)
-        const float tol = (SIGMOID ? 2e-6f : 1.5e-5f) * warp_max(smax) +
+      const uint32_t next = __reduce_max_sync(kFull, value);
+      if (next > kShut) {  // the last kept value against the first that is not kept
+        const float in = order_value(last), out = order_value(next);
+        // four scores of at most 1 (rden) each; |x| e^-|x| is below 0.4
+        const float tol = (SIGMOID ? 4e-6f : 1.5e-5f * rden) +
                           5e-7f * fmaxf(fabsf(in), fabsf(out)) + 1e-36f;
         sure = in - out > tol;
       }
+      if (whole) {
+        if (!((kept >> my_group) & 1u)) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (e0 + i < E && !((kept >> (whole ? my_group : (e0 + i) / n)) & 1u)) key[i] = kShut;
-        // inside the kept groups, without bias, the score rises with the logit
-        if (p.bias == nullptr && key[i] != kShut) key[i] = order_bits(z[i]);
+          for (int i = 0; i < VPL; ++i) key[i] = kShut;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (e0 + i < E && !((kept >> ((e0 + i) / n)) & 1u)) key[i] = kShut;
+      }
+      if (p.bias == nullptr) {  // inside the kept groups the score rises with the logit
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (key[i] != kShut) key[i] = order_bits(z[i]);
       }
     }
     int mine = -1;             // expert of slot `lane`
@@ -427,7 +441,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       const float s2 = __shfl_down_sync(kFull, s, 1), z2 = __shfl_down_sync(kFull, zj, 1);
       const int m2 = __shfl_down_sync(kFull, mine, 1);
       if (lane < k && mine >= 0 && lane < 31 && m2 >= 0) {
-        const float rel = SIGMOID ? 1e-6f : 7e-6f + 1.3e-7f * (zmax - fminf(zj, z2));
+        const float x = SIGMOID ? fmaxf(fabsf(zj), fabsf(z2)) : zmax - fminf(zj, z2);
+        const float rel = SIGMOID ? 1.5e-6f + 1.3e-7f * x : 7e-6f + 2.6e-7f * x;
         const float tol = rel * fmaxf(s, s2) + 2.5e-7f * fmaxf(fabsf(c), fabsf(c2)) + 1e-36f;
         if (c - c2 <= tol && !(zj == z2 && b == b2)) sure = false;
       }
@@ -479,8 +494,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       // relative to the largest chosen score: no underflow of all of them
       const float zc = warp_max(zj);
       if (mine >= 0) s = SIGMOID ? sigmoid_scaled(zj, fminf(zc, 0.0f)) : expf(zj - zc);
-      const float sum = warp_sum(s);
-      if (mine >= 0) s = s / sum;
+      const float sum = warp_sum(s);  // between 1/2 and 32
+      s = mine >= 0 ? __fdividef(s, sum) : 0.0f;
     } else if constexpr (SIGMOID) {
       if (mine >= 0) s = sigmoid_scaled(zj, 0.0f);
     } else {
@@ -491,8 +506,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       if (mine >= 0) s = expf(zj - zmax) / den;
     }
     if (slot) {
-      p.idx[(size_t)t * k + lane] = mine;
-      p.w[(size_t)t * k + lane] = mine >= 0 ? s * p.scale : 0.0f;
+      p.idx[t * k + lane] = mine;
+      p.w[t * k + lane] = mine >= 0 ? s * p.scale : 0.0f;
     }
   }
 }
@@ -639,18 +654,19 @@ __global__ void __launch_bounds__(256) route_grad_dense_kernel(const RouteGradPa
   const int e0 = lane * VPL;
   pdl_wait();
   pdl_trigger();
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.T; t += gridDim.x * 8) {
+  for (long long t = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); t < p.T;
+       t += (long long)gridDim.x * 8) {
     const size_t row = (size_t)t * E;
     float v[VPL];  // then exp(z - zmax) of the lane's experts (0: not finite)
     load_row<DT, VPL>(p.logits, row, e0, E, v);
-    int e = lane < k ? __ldg(p.idx + (size_t)t * k + lane) : -1;
+    int e = lane < k ? __ldg(p.idx + t * k + lane) : -1;
     if (e >= E) {
       raise_status(p.status, LRMOE_ST_BAD_EXPERT);
       e = -1;
     }
     const float z = e >= 0 ? load_logit<DT>(p.logits, row + e) : -INFINITY;
     if (!(fabsf(z) < INFINITY)) e = -1;  // NaN and +inf are flagged with the row
-    const float dw = e >= 0 ? __ldg(p.dw + (size_t)t * k + lane) : 0.0f;
+    const float dw = e >= 0 ? __ldg(p.dw + t * k + lane) : 0.0f;
     float m = -INFINITY;
     bool bad = false;
 #pragma unroll
@@ -692,18 +708,27 @@ __global__ void __launch_bounds__(256) route_grad_dense_kernel(const RouteGradPa
 }
 
 template <lrmoe_dtype DT, bool SIGMOID>
-cudaError_t route_by_width(const RouteParams& p, cudaStream_t s) {
+cudaError_t route_by_width(RouteParams p, cudaStream_t s) {
   auto kern = route_kernel<DT, SIGMOID, 32>;
-  if (p.E <= 32)
+  int vpl = 32;  // experts of a lane
+  if (p.E <= 32) {
     kern = route_kernel<DT, SIGMOID, 1>;
-  else if (p.E <= 64)
+    vpl = 1;
+  } else if (p.E <= 64) {
     kern = route_kernel<DT, SIGMOID, 2>;
-  else if (p.E <= 128)
+    vpl = 2;
+  } else if (p.E <= 128) {
     kern = route_kernel<DT, SIGMOID, 4>;
-  else if (p.E <= 256)
+    vpl = 4;
+  } else if (p.E <= 256) {
     kern = route_kernel<DT, SIGMOID, 8>;
-  else if (p.E <= 512)
+    vpl = 8;
+  } else if (p.E <= 512) {
     kern = route_kernel<DT, SIGMOID, 16>;
+    vpl = 16;
+  }
+  p.n = p.E / p.groups;
+  p.lpg = p.n % vpl == 0 ? p.n / vpl : 0;
   const bool plain = p.bias == nullptr && p.groups == 1;
   const size_t smem = plain ? 0 : sizeof(double) * (size_t)kRouteWarps * p.E;  // <= 32 KB
   long long blocks = ((long long)p.T + kRouteWarps - 1) / kRouteWarps;
@@ -761,7 +786,7 @@ cudaError_t route_grad_by_fn(const RouteGradParams& p, bool sigmoid, bool renorm
 cudaError_t launch_route(const void* logits, int T, int E, lrmoe_dtype dt, const float* bias, int k,
                          lrmoe_score_fn fn, int n_group, int topk_group, int renorm, float scale,
                          int32_t* idx, float* w, uint32_t* status, cudaStream_t s) {
-  const RouteParams p{logits, bias, T, E, k, n_group, topk_group, renorm, scale, idx, w, status};
+  const RouteParams p{logits, bias, T, E, k, n_group, topk_group, renorm, 0, 0, scale, idx, w, status};
   const bool sg = fn == LRMOE_SCORE_SIGMOID;
   if (dt == LRMOE_BF16)
     return sg ? route_by_width<LRMOE_BF16, true>(p, s) : route_by_width<LRMOE_BF16, false>(p, s);

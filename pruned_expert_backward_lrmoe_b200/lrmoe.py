@@ -144,10 +144,9 @@ def _arg(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple,
         return None
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name}: expected a CUDA tensor on one device with the others, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor on one device with the others, "
+                         f"got {t.device}, strides {t.stride()}")
     return t.data_ptr()
 
 
@@ -157,12 +156,12 @@ def _status(t: Optional[torch.Tensor], dev: int):
 
 def _launch(dev: int, stream):
     """The stream of a call whose tensors are on device `dev`, which must be the current one."""
-    if dev != torch.cuda.current_device():
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on cuda:{dev}, the call is made on "
                          f"cuda:{torch.cuda.current_device()}")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 # ---------------------------------------------------------------------------

@@ -196,8 +196,10 @@ def test_binding_refuses_types_and_shapes(lib):
     refused("bias", L.lrmoe_route, z, i, w, bias=c(torch.zeros(15)))
     refused("status", L.lrmoe_route, z, i, w, status=c(torch.zeros(1)))
     refused("contiguous", L.lrmoe_route, c(torch.zeros(16, 4)).t(), i, w)
-    refused("CUDA tensor", L.lrmoe_route, torch.zeros(4, 16), i, w)
-    refused("CUDA tensor", L.lrmoe_route, z, i, torch.zeros(4, 2))
+    refused("one device", L.lrmoe_route, torch.zeros(4, 16), i, w)
+    refused("one device", L.lrmoe_route, z, i, torch.zeros(4, 2))
+    refused("CUDA tensors", L.lrmoe_route, torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32),
+            torch.zeros(4, 2))
     refused("dlogits", L.lrmoe_route_grad, z, i, w, c(z.bfloat16()))
     x, W, off = c(torch.zeros(4, 64)), c(torch.zeros(3, 32, 64)), c(torch.zeros(4, dtype=torch.int32))
     perm, new = c(torch.zeros(8, dtype=torch.int32)), lambda *s: c(torch.zeros(*s))
@@ -221,6 +223,7 @@ def test_binding_refuses_tensors_of_another_device(monkeypatch):
     with pytest.raises(ValueError, match="one device"):
         L._arg("w", far, torch.float32, (4, 2), 0)
     assert L._arg("w", far, torch.float32, (4, 2), 1) == far.data_ptr()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="cuda:1"):
         L._launch(1, None)

@@ -150,6 +150,24 @@ def test_route_many_tokens_and_repeat():
     np.testing.assert_array_equal(a[0], want.numpy())
 
 
+def test_route_offsets_past_32_bits():
+    """More than 2^31 logits: the last tokens read and write the right rows."""
+    T, E, k = 4194310, 513, 2
+    z = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    z[-4:, 500], z[-4:, 7] = 9.0, 8.0
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    L.lrmoe_route(z, idx, w, renormalise=False, score_fn=L.LRMOE_SCORE_SIGMOID)
+    assert idx[-4:].tolist() == [[500, 7]] * 4 and idx[-5].tolist() == [0, 1]
+    assert bool((idx[:-4] == torch.tensor([0, 1], device="cuda")).all())
+    dw = torch.zeros(T, k, device="cuda")
+    dw[-1] = 1.0
+    dz = torch.full_like(z, float("nan"))
+    for renorm, fn in ((False, L.LRMOE_SCORE_SIGMOID), (False, L.LRMOE_SCORE_SOFTMAX)):
+        L.lrmoe_route_grad(z, idx, dw, dz, renormalise=renorm, score_fn=fn)
+        assert not bool(dz[:-1].any()) and bool(dz[-1, 500] != 0) and not bool(dz.isnan().any())
+
+
 # ---------------------------------------------------------------------------
 # gradient
 # ---------------------------------------------------------------------------
