@@ -536,7 +536,7 @@ __device__ __forceinline__ void store_row(void* z, size_t row, int e0, int E, co
 #pragma unroll
       for (int i = 0; i < kBytes / 4; ++i) {
         if constexpr (DT == LRMOE_BF16)
-          w[i] = f32_to_bf16_bits_rne(v[2 * i]) | (f32_to_bf16_bits_rne(v[2 * i + 1]) << 16);
+          w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
         else
           w[i] = __float_as_uint(v[i]);
       }
@@ -558,6 +558,29 @@ __device__ __forceinline__ void store_row(void* z, size_t row, int e0, int E, co
     else
       static_cast<float*>(z)[row + e0 + i] = v[i];
   }
+}
+
+// An expert named by several slots: the first of them gets the sum over all, in slot order.  `tag`
+// tells the experts of the warp's tokens apart; lanes without a slot have e < 0.  True for the
+// lanes that write their expert's value.
+__device__ __forceinline__ bool first_of_slots(int e, float& d, int tag, int lane) {
+  const unsigned same = __match_any_sync(kFull, e >= 0 ? tag : ~lane);
+  if (!__any_sync(kFull, (same & (same - 1u)) != 0u)) return e >= 0;
+  const float own = d;
+  d = 0.0f;
+  for (int i = 0; i < 32; ++i) {
+    const float di = __shfl_sync(kFull, own, i);
+    if ((same >> i) & 1u) d += di;
+  }
+  return e >= 0 && lane == __ffs(same) - 1;
+}
+
+template <lrmoe_dtype DT>
+__device__ __forceinline__ void store_logit(void* z, size_t i, float v) {
+  if constexpr (DT == LRMOE_BF16)
+    static_cast<unsigned short*>(z)[i] = (unsigned short)f32_to_bf16_bits_rne(v);
+  else
+    static_cast<float*>(z)[i] = v;
 }
 
 // One token's slots, slot j in lane j of the token's SUB lanes:
@@ -622,31 +645,15 @@ __global__ void __launch_bounds__(256) route_grad_sparse_kernel(const RouteGradP
     } else {
       if (e >= 0) d = p.scale * dw * sigmoid_scaled(z, 0.0f) * sigmoid_scaled(-z, 0.0f);
     }
-    // An expert named by several slots: the first of them adds the others, in slot order.  Lanes
-    // without a slot have a number of their own.
-    const unsigned same = __match_any_sync(kFull, e >= 0 ? (sub << 16) | e : ~lane);
-    bool write = e >= 0;
-    if (__any_sync(kFull, (same & (same - 1u)) != 0u)) {
-      const float own = d;
-      d = 0.0f;
-      for (int i = 0; i < 32; ++i) {
-        const float di = __shfl_sync(kFull, own, i);
-        if ((same >> i) & 1u) d += di;
-      }
-      write = write && lane == __ffs(same) - 1;
-    }
+    const bool write = first_of_slots(e, d, (sub << 16) | e, lane);
     __syncwarp();  // the zeros are written before the values
-    if (write) {
-      if constexpr (DT == LRMOE_BF16)
-        static_cast<unsigned short*>(p.dlogits)[row + e] = (unsigned short)f32_to_bf16_bits_rne(d);
-      else
-        static_cast<float*>(p.dlogits)[row + e] = d;
-    }
+    if (write) store_logit<DT>(p.dlogits, row + e, d);
   }
 }
 
 // Softmax, not renormalised: every logit gets a gradient,
-//   dz_e = s_e (scale sum of dw over the slots of e - scale sum_i dw_i s_i).
+//   dz_e = s_e (scale sum of dw over the slots of e - scale sum_i dw_i s_i):
+// the row as if no slot named an expert, then the slots' experts again.
 template <lrmoe_dtype DT, int VPL>
 __global__ void __launch_bounds__(256) route_grad_dense_kernel(const RouteGradParams p) {
   const int lane = threadIdx.x & 31;
@@ -687,23 +694,16 @@ __global__ void __launch_bounds__(256) route_grad_dense_kernel(const RouteGradPa
     }
     sum = warp_sum(sum);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-    const float dot = warp_sum(e >= 0 ? dw * (expf(z - zmax) * inv) : 0.0f);
-    float acc[VPL];
+    const float sj = e >= 0 ? expf(z - zmax) * inv : 0.0f;
+    const float dot = warp_sum(dw * sj);
+    const float rest = -p.scale * dot * inv;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] = -dot;
-    for (int j0 = 0; j0 < k; j0 += 8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {  // lanes past k hold no expert
-        const int at = __shfl_sync(kFull, e, j0 + j) - e0;
-        const float dj = __shfl_sync(kFull, dw, j0 + j);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (at == i) acc[i] += dj;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] = v[i] * inv * (p.scale * acc[i]);
-    store_row<DT, VPL>(p.dlogits, row, e0, E, acc);
+    for (int i = 0; i < VPL; ++i) v[i] *= rest;
+    store_row<DT, VPL>(p.dlogits, row, e0, E, v);
+    float d = dw;
+    const bool write = first_of_slots(e, d, e, lane);
+    __syncwarp();  // the row is written before the slots' values
+    if (write) store_logit<DT>(p.dlogits, row + e, sj * (p.scale * (d - dot)));
   }
 }
 
