@@ -26,6 +26,8 @@ SIZES = {
     "dense": [300],
     "small": [3, 0, 60, 7],
     "none": [0, 0, 0],
+    # long experts, with and without a last tile of at most 128 rows, an empty one between
+    "long": [700, 1029, 0, 2050, 257, 3841, 512, 1153, 640, 4100],
 }
 
 
@@ -144,6 +146,24 @@ def test_swiglu_gathered(sizes, H, I, k, bias, outputs, dt):
 def test_swiglu_gathered_long_rows(H, I):
     """Long K (wide tiles): one, two and three column blocks."""
     test_swiglu_gathered("edges", H, I, 4, True, "gua", "bf16")
+
+
+@pytest.mark.parametrize("H,I", [(64, 1160), (2048, 1160), (136, 2184)])
+def test_swiglu_long_experts(H, I):
+    test_swiglu_gathered("long", H, I, 4, True, "gua", "bf16")
+
+
+@pytest.mark.parametrize("K,N", [(64, 2056), (136, 4104)])
+@pytest.mark.parametrize("extras", ["plain", "all", "in place"])
+def test_linear_long_experts(K, N, extras):
+    test_linear("long", K, N, extras, "bf16")
+
+
+@pytest.mark.parametrize("sizes", [[4096] * 4, [4097] * 4, [16500], [3, 20000, 5]])
+def test_linear_with_uneven_last_tiles(sizes):
+    """No last tile at all, one in every expert, one expert that holds nearly all rows."""
+    SIZES["here"] = sizes
+    test_linear("here", 72, 2056, "all", "bf16")
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
