@@ -537,8 +537,9 @@ int lrmoe_route_grad(const void* logits, int T, int E, lrmoe_dtype dt, const int
  *   W_down), db [E][N] fp32, zeros for an empty expert; accumulate = 1 adds to
  *   db.  fp32 sums in a fixed order.
  *
- * perm entries out of range set LRMOE_ST_BAD_INDEX and that row's outputs are
- * left unwritten; perm must not name a row twice.  Output rows that no packed
+ * Of perm only the entries of rows below offsets[E] are read; those out of range
+ * set LRMOE_ST_BAD_INDEX and that row's outputs are left unwritten; perm must
+ * not name a row twice.  Output rows that no packed
  * row names are left as they were.  Apart from residual = out, outputs must not
  * overlap inputs or one another.  E <= 1024.
  * ------------------------------------------------------------------------- */

@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "../../include/lrmoe.h"
+#include "forward.h"
 #include "launch.h"
 
 namespace lrmoe {

@@ -13,6 +13,7 @@
 // memory, each in a fixed order.  No atomics, no workspace.  65536 rows of 1536 over 128 experts:
 // 38 us, 5.3 TB/s (plain 16-byte loads, eight in flight: 59 us); 16381 rows of 4096 of one expert:
 // 27 us, 4.9 TB/s.
+#include "forward.h"
 #include "gemm_common.cuh"
 
 namespace lrmoe {

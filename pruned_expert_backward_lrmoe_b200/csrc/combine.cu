@@ -7,6 +7,7 @@
 // once, in 16-byte vectors, eight of a token's rows in flight together per lane.  T = 16384, top-8,
 // H = 4096, residual: 222 us, 5.9 TB/s.
 #include "common.cuh"
+#include "forward.h"
 #include "launch.h"
 
 namespace lrmoe {

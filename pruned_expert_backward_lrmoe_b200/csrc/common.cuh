@@ -238,16 +238,6 @@ __device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gsrc, ui
                : "memory");
 }
 
-// This thread's copies since the last commit become a group; wait until at most N groups are
-// still in flight.
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait_group() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Wait until every cp.async this thread issued has landed.
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");

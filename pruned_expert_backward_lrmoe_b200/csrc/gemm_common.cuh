@@ -303,20 +303,6 @@ bool make_map_3d(CUtensorMap* m, const void* base, uint64_t E, uint64_t K, uint6
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3D bf16 map over [E][N][K] (K-major weights of the forward products), box = 64 (K) x 128 (N)
-// x 1, 128-B swizzle.
-bool make_map_kmajor(CUtensorMap* m, const void* base, uint64_t E, uint64_t N, uint64_t K) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {K, N, E};
-  cuuint64_t strides[2] = {K * 2, N * K * 2};
-  cuuint32_t box[3] = {64, 128, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // 3D fp32 map over dW [E][N1][N2], box = 32 (N2) x 32 (N1) x 1, 128-B swizzle (store side).
 bool make_map_out_f32(CUtensorMap* m, void* base, uint64_t E, uint64_t N1, uint64_t N2) {
   EncodeTiledFn fn = encode_fn();

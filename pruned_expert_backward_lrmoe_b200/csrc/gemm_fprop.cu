@@ -44,6 +44,7 @@
 //     4096 product: 161 us, cuBLAS 151, without epilogue 143.
 //   SwiGLU, T = 16 (a few rows per expert), H = 2048, I = 768: 80-85 us, the weights of the experts
 //     taken at 6.2-6.6 TB/s (HBM).
+#include "forward.h"
 #include "gemm_common.cuh"
 
 namespace lrmoe {
@@ -67,6 +68,20 @@ struct FpropParams {
   int rows_cap;
   int wide;                 // outputs' rows start on 32 bytes and N % 16 == 0
 };
+
+// 3D bf16 map over [E][N][K] (K-major weights of the forward products), box = 64 (K) x 128 (N)
+// x 1, 128-B swizzle.
+bool make_map_kmajor(CUtensorMap* m, const void* base, uint64_t E, uint64_t N, uint64_t K) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {K, N, E};
+  cuuint64_t strides[2] = {K * 2, N * K * 2};
+  cuuint32_t box[3] = {64, 128, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // DOUBLE: a PAIR tile of 256 rows x 512 columns (both accumulators at once, see fprop_kernel).
 template <bool PAIR, bool DOUBLE>

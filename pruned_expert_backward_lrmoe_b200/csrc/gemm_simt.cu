@@ -7,6 +7,7 @@
 // 16-deep K slices, 4x4 outputs per thread, persistent grid over a tile table
 // built on the device from `offsets`).
 #include "common.cuh"
+#include "forward.h"
 #include "grouped.cuh"
 #include "launch.h"
 
@@ -153,6 +154,16 @@ __global__ void __launch_bounds__(NT) wgrad_simt_kernel(
       }
     }
   }
+}
+
+// This thread's copies since the last commit become a group; wait until at most N groups are
+// still in flight.
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Forward products against K-major weights: D[r][n] = sum_k A[r][k] W[e][n][k] for r in R_e.

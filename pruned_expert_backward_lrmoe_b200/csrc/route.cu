@@ -23,6 +23,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "forward.h"
 #include "launch.h"
 
 namespace lrmoe {
