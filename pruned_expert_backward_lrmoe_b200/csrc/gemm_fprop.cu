@@ -23,16 +23,17 @@
 // rows to a one-SM tile in a second launch that overlaps the first one's drain.
 //
 // Gathered rows come in by four-row TMA gathers, which the copy engine takes about 19 ns each
-// (32 a K block and CTA: more than the block's products take).  So with a long K a PAIR tile is
-// DOUBLE: 256 rows x 512 columns, both accumulators at once, half the gathers per product; else
-// the two accumulators alternate and a tile's epilogue runs under the next tile's products.
+// (32 a K block and CTA: more than the block's products take).  So their PAIR tile is DOUBLE: 256
+// rows x 512 columns, both accumulators at once, half the gathers per product.  For packed rows
+// (and on one SM) the two accumulators alternate and a tile's epilogue runs under the next
+// tile's products.  Single against DOUBLE, I = 768, T = 8192, gathered: H = 256 164 and 147 us,
+// 1024 315 and 300, T = 16384 H = 4096 I = 1408 3.07 and 2.86 ms; packed 2.53 and 2.70 ms.
 //
 // Every tile has the same K depth, so tiles are dealt out in turn; there is no device-side
 // scheduling state that two launches or two captured graphs could share.
 //
-// Roles: producer warps (one for packed rows; to gather, eight of a PAIR launch and four of a
-// one-SM launch share the four-row gathers: with one warp the T = 16384 layer below took 6.8 ms),
-// one warp for tensor memory and MMA issue, eight epilogue warps.  Every wait is bounded
+// Roles: producer warps (one for packed rows; to gather, four share the four-row
+// gathers: with one warp the T = 16384 layer below took 6.8 ms), one warp for tensor memory and MMA issue, eight epilogue warps.  Every wait is bounded
 // (LRMOE_ST_TIMEOUT, then a clean exit).  No TMA multicast.
 //
 // What bounds it, and what it measured (B200, under load until the power cap settles):
@@ -195,15 +196,16 @@ __device__ __forceinline__ void add_row32(uint32_t (&r)[32], const uint16_t* v, 
   }
 }
 
-// Producer warps.  Packed rows need one; gathered rows come in through several, since a warp's
-// four-row loads issue one after another (about 40 ns each).
-template <bool PAIR, bool GATHER>
-constexpr int kProducers = GATHER ? (PAIR ? 8 : 4) : 1;
-template <bool PAIR, bool GATHER>
-constexpr int kFwdThreads = 32 * (kProducers<PAIR, GATHER> + 1 + kEpiWarps);
+// Producer warps.  Packed rows need one; gathered rows come in through four, since a warp's
+// four-row loads issue one after another (about 40 ns each; eight warps cost the epilogue its
+// registers: H = 2048, I = 768, T = 8192 549 us against 531).
+template <bool GATHER>
+constexpr int kProducers = GATHER ? 4 : 1;
+template <bool GATHER>
+constexpr int kFwdThreads = 32 * (kProducers<GATHER> + 1 + kEpiWarps);
 
 template <bool SWIGLU, bool PAIR, bool GATHER, bool DOUBLE>
-__global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
+__global__ void __launch_bounds__(kFwdThreads<GATHER>, 1) fprop_kernel(
     const __grid_constant__ CUtensorMap tmA /* rows: 32-row boxes, or one-row boxes to gather */,
     const __grid_constant__ CUtensorMap tmB /* W [E][rows][K], 128-row boxes */,
     const FpropParams p) {
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(kFwdThreads<PAIR, GATHER>, 1) fprop_kernel(
   constexpr int STAGES = L::kStages;
   constexpr int BN = kBNT;
   constexpr int kTileM = PAIR ? 2 * BM : BM;
-  constexpr int NP = kProducers<PAIR, GATHER>;
+  constexpr int NP = kProducers<GATHER>;
   const int E = p.E;
   uint32_t* status = p.status;
   extern __shared__ uint8_t smem_raw[];
@@ -623,7 +625,7 @@ cudaError_t launch_fprop(const CUtensorMap& a, const CUtensorMap& b, FpropParams
   const int nt = (prm.N + feat - 1) / feat;
   long long tiles = ((long long)prm.rows_cap / tile_m + prm.E) * nt;  // an upper bound
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kFwdThreads<PAIR, GATHER>);
+  cfg.blockDim = dim3(kFwdThreads<GATHER>);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -658,18 +660,7 @@ cudaError_t fprop(const void* rows, int n_rows, const void* W, int w_rows, Fprop
   const bool pairs = prm.rows_cap > BM;
   if (pairs) {
     prm.part = kRowsPairs;
-    cudaError_t e;
-    if constexpr (GATHER) {
-      // DOUBLE halves the gathered rows per flop, but a tile's epilogue is not overlapped by the
-      // next tile's products: worth it over long K.  T = 16384, H = 4096, I = 1408: 2.86 ms
-      // against 3.07; H = 2048, I = 768, T = 8192: 0.58 against 0.60.  (Packed rows: 2.70 against
-      // 2.53, so they keep the single tile.)
-      const bool twice = prm.K >= 2048 && prm.N > kFeat<SWIGLU>;
-      e = twice ? launch_fprop<SWIGLU, true, true, true>(a, b, prm, s)
-                : launch_fprop<SWIGLU, true, true, false>(a, b, prm, s);
-    } else {
-      e = launch_fprop<SWIGLU, true, false, false>(a, b, prm, s);
-    }
+    const cudaError_t e = launch_fprop<SWIGLU, true, GATHER, GATHER>(a, b, prm, s);
     if (e != cudaSuccess) return e;
   }
   prm.part = pairs ? kRowsTails : kRowsAll;
