@@ -189,7 +189,7 @@ struct FpropF32 {
 
 // 128 CUDA-core multiply-adds a cycle and SM are the limit for large layers; the layers that fp32
 // is for are small, and there the latency of a tile is: T = 1021, K = 256, N = 512, one expert,
-// residual: 19 us.
+// residual: 16 us.
 //
 // Ring of FS 16-deep K slices, copied asynchronously as they lie in memory; rows of 20 floats keep
 // the 16-byte reads of neighbouring columns in different banks.
@@ -200,10 +200,18 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
 
-// TN: tile columns.  64, or 32 where 64-column tiles would leave SMs without one.
+// A thread makes RI rows x TN / 16 columns of the 64 x TN tile: the more, the fewer reads of
+// shared memory per product, which is what bounds the slices (4 x 4 per thread: 143 us where
+// 8 x 4 takes 125).
+constexpr int RI = 8;
+constexpr int TY = BM / RI;   // thread rows
+constexpr int FT = 16 * TY;   // threads
+constexpr int LR = FT / 4;    // tile rows that the threads load in a pass
+
 template <int TN>
-__global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
+__global__ void __launch_bounds__(FT) fprop_simt_kernel(const FpropF32 p) {
   constexpr int CJ = TN / 16;  // columns of a thread
+  constexpr int AL = BM / LR, BL = TN > LR ? TN / LR : 1;
   __shared__ int tstart[kMaxExperts + 1];
   __shared__ int scratch[33];
   __shared__ __align__(16) float As[FS][BM][FP];
@@ -245,27 +253,37 @@ __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
       dest[tid] = d;
     }
     __syncthreads();
-    // weight row behind column lr of the tile
-    int wrow = n0 + lr;
-    bool wok = lr < TN && wrow < N;
-    if (p.swiglu) {
-      wrow = n0 + lr % (TN / 2);
-      wok = lr < TN && wrow < N;
-      wrow += lr >= TN / 2 ? N : 0;
+    const float* ap[AL];  // this thread's rows of A and of W (nullptr: zeros)
+    const float* wp[BL];
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      const int s = src[lr + i * LR];
+      ap[i] = s < 0 ? nullptr : p.rows + (size_t)s * K;
     }
-    const float* wp = p.W + ((size_t)e * (p.swiglu ? 2 * N : N) + (wok ? wrow : 0)) * K;
-    const int s = src[lr];
-    const float* ap = p.rows + (size_t)(s < 0 ? 0 : s) * K;
-    uint64_t acc2[4][CJ] = {};  // sums over even k (low word) and odd k (high word)
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      const int c = lr + i * LR;  // column of the tile
+      int w = p.swiglu ? n0 + c % (TN / 2) : n0 + c;
+      const bool ok = c < TN && w < N;
+      if (p.swiglu && c >= TN / 2) w += N;
+      wp[i] = ok ? p.W + ((size_t)e * (p.swiglu ? 2 * N : N) + w) * K : nullptr;
+    }
+    uint64_t acc2[RI][CJ] = {};  // sums over even k (low word) and odd k (high word)
     const int steps = (K + BK - 1) / BK;
-    auto fetch = [&](int step) {  // this thread's 16 bytes of A and B (K % 4 == 0), or zeros
-      const int k0 = step * BK;
-      const bool ok = k0 + lk < K;
-      const int f = step % FS;
+    auto fetch = [&](int step) {  // this thread's 16-byte pieces of a slice (K % 4 == 0)
+      const int k = step * BK + lk, f = step % FS;
       if (step < steps) {
-        cp_async_16(&As[f][lr][lk], s >= 0 && ok ? ap + k0 + lk : p.rows, s >= 0 && ok ? 16 : 0);
-        if (lr < TN)
-          cp_async_16(&Bs[f][lr][lk], wok && ok ? wp + k0 + lk : p.W, wok && ok ? 16 : 0);
+#pragma unroll
+        for (int i = 0; i < AL; ++i) {
+          const bool ok = ap[i] && k < K;
+          cp_async_16(&As[f][lr + i * LR][lk], ok ? ap[i] + k : p.rows, ok ? 16 : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < BL; ++i) {
+          const bool ok = wp[i] && k < K;
+          if (lr + i * LR < TN)
+            cp_async_16(&Bs[f][lr + i * LR][lk], ok ? wp[i] + k : p.W, ok ? 16 : 0);
+        }
       }
       cp_async_commit();
     };
@@ -278,33 +296,33 @@ __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
       const int f = step % FS;
 #pragma unroll
       for (int kk = 0; kk < BK; kk += 4) {
-        ulonglong2 av[4], bv[CJ];  // (k, k + 1), (k + 2, k + 3)
+        ulonglong2 av[RI], bv[CJ];  // (k, k + 1), (k + 2, k + 3)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          av[i] = *reinterpret_cast<const ulonglong2*>(&As[f][ty + 16 * i][kk]);
+        for (int i = 0; i < RI; ++i)
+          av[i] = *reinterpret_cast<const ulonglong2*>(&As[f][ty + TY * i][kk]);
 #pragma unroll
         for (int j = 0; j < CJ; ++j)
           bv[j] = *reinterpret_cast<const ulonglong2*>(&Bs[f][tx + 16 * j][kk]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RI; ++i)
 #pragma unroll
           for (int j = 0; j < CJ; ++j) fma2(acc2[i][j], av[i].x, bv[j].x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RI; ++i)
 #pragma unroll
           for (int j = 0; j < CJ; ++j) fma2(acc2[i][j], av[i].y, bv[j].y);
       }
     }
-    float acc[4][CJ];
+    float acc[RI][CJ];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RI; ++i)
 #pragma unroll
       for (int j = 0; j < CJ; ++j)
         acc[i][j] = __uint_as_float((uint32_t)acc2[i][j]) + __uint_as_float((uint32_t)(acc2[i][j] >> 32));
     // columns tx + 16 j of the tile: SwiGLU holds gate features tx (and tx + 16) and their ups
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = ty + 16 * i;
+    for (int i = 0; i < RI; ++i) {
+      const int m = ty + TY * i;
       const int d = dest[m];
       if (d < 0) continue;
       const size_t at = (size_t)d * N;
@@ -340,16 +358,17 @@ __global__ void __launch_bounds__(NT) fprop_simt_kernel(const FpropF32 p) {
 }
 
 cudaError_t fprop_simt(const FpropF32& p, cudaStream_t s) {
-  // upper bounds of the tile counts; with under two 64-column tiles per SM the narrow ones spread
-  // better (T = 1021, K = 256, N = 512, one expert: 20 us against 23)
-  auto tiles = [&](int tn) {
+  auto tiles = [&](int tn) {  // an upper bound
     const int feat = p.swiglu ? tn / 2 : tn;
     return ((long long)p.rows_cap / BM + p.E) * ((p.N + feat - 1) / feat);
   };
-  const bool narrow = tiles(64) < 2ll * num_sms();
-  const long long n = tiles(narrow ? 32 : 64), cap = 4ll * num_sms();
+  // 64-column tiles do more products per read of shared memory, 32-column ones spread a small
+  // product over more SMs: 8192 x 512 x 512 125 and 134 us, 2048 x 256 x 256 over four experts 19.4
+  // and 16.3.
+  const bool narrow = tiles(64) < 4ll * num_sms();
+  const long long n = tiles(narrow ? 32 : 64), cap = 8ll * num_sms();
   auto kern = narrow ? fprop_simt_kernel<32> : fprop_simt_kernel<64>;
-  return launch_pdl(kern, dim3((unsigned)(n < cap ? n : cap)), dim3(NT), 0, s, p);
+  return launch_pdl(kern, dim3((unsigned)(n < cap ? n : cap)), dim3(FT), 0, s, p);
 }
 
 }  // namespace
