@@ -9,9 +9,9 @@
 //
 // The order is that of keys computed in fp64, not of one fp32 rounding of them.  Without bias
 // the score rises with the logit, so the logits themselves are compared.  Keys with a bias and
-// group values are computed in fp32 with a bound on their error; where two neighbours in the order are nearer than
-// that bound (about one token in a thousand) and are not the same logit and bias, the warp
-// computes the keys of that token again in fp64 and selects by those.
+// group values are computed in fp32 with a bound on their error; where that leaves the order open
+// (about one token in a thousand), the warp computes the keys of that token again in fp64 and
+// selects by those.
 //
 // One warp per token.  Expert e = lane * VPL + i lives in register i of a lane, so the lowest
 // lane that holds a maximum holds the lowest expert.
@@ -200,11 +200,13 @@ __device__ __noinline__ int topk_fp64(double* key, int E, int k, int lane) {
 // The k experts of the largest keys in slot order, by threshold: at least k + 1 of the warp's keys
 // reach the (k + 1)-th largest of the 32 lane maxima, and few more do (11 or so of 128 for
 // k = 8).  Those that do are brought to one per lane and ranked by counting (key, lower
-// expert first).  Lane j gets slot j (mine, mine_key), lane k the best one left.  False (nothing
-// set) where more than 32 reach the threshold.
+// expert first).  Lane j gets the j-th largest (mine, mine_key), for all that reach the threshold;
+// whole: no expert is left behind them.
+// False (nothing set) where more than 32 do.
 template <int VPL>
 __device__ __forceinline__ bool topk_by_threshold(const uint32_t (&key)[VPL], int k, int lane,
-                                                  uint64_t* box, int& mine, uint32_t& mine_key) {
+                                                  uint64_t* box, int& mine, uint32_t& mine_key,
+                                                  bool& whole) {
   uint32_t best = key[0];
 #pragma unroll
   for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
@@ -219,7 +221,8 @@ __device__ __forceinline__ bool topk_by_threshold(const uint32_t (&key)[VPL], in
       if (top) left = 0u;
     }
   }
-  if (bar <= kShut) bar = kShut + 1u;  // fewer lanes than that hold a key: take all keys
+  whole = bar <= kShut;  // fewer lanes than that hold a key: take all keys
+  if (whole) bar = kShut + 1u;
   int count = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -243,7 +246,7 @@ __device__ __forceinline__ bool topk_by_threshold(const uint32_t (&key)[VPL], in
   __syncwarp();
   if (lane < count) box[rank] = own;
   __syncwarp();
-  if (lane < count && lane <= k) {
+  if (lane < count) {
     const uint64_t got = box[lane];
     mine = (int)~(uint32_t)got;
     mine_key = (uint32_t)(got >> 32);
@@ -255,13 +258,15 @@ __device__ __forceinline__ bool topk_by_threshold(const uint32_t (&key)[VPL], in
 // The same in k + 1 rounds: the warp's largest key, its lowest holder, gone for the next round.
 template <int VPL>
 __device__ __noinline__ void topk_by_rounds(uint32_t (&key)[VPL], int k, int lane, int& mine,
-                                            uint32_t& mine_key) {
+                                            uint32_t& mine_key, bool& whole) {
+  whole = false;
   for (int j = 0; j < (k < 31 ? k + 1 : 32); ++j) {
     uint32_t best = key[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
     const uint32_t top = __reduce_max_sync(kFull, best);
-    if (top <= kShut) break;
+    whole = top <= kShut;
+    if (whole) break;
     const int owner = __ffs(__ballot_sync(kFull, best == top)) - 1;
     int at = 0;
     if (lane == owner) {
@@ -298,6 +303,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
   // this lane's biases; one that is not finite shuts its expert
   float bias[VPL];
   bool bad_bias = false;
+  float low_bias = INFINITY;  // the lowest finite one
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     bias[i] = p.bias != nullptr && e0 + i < E ? __ldg(p.bias + e0 + i) : 0.0f;
@@ -305,7 +311,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       bad_bias = true;
       bias[i] = -INFINITY;
     }
+    if (e0 + i < E && bias[i] > -INFINITY) low_bias = fminf(low_bias, bias[i]);
   }
+  if (p.bias != nullptr) low_bias = -warp_max(-low_bias);
   // 64-bit: T may be near 2^31
   for (long long t = (long long)blockIdx.x * kRouteWarps + warp; t < p.T;
        t += (long long)gridDim.x * kRouteWarps) {
@@ -324,10 +332,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
     }
     if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
     if (!SIGMOID && !(plain && p.renorm)) zmax = warp_max(zmax);
-    // Order keys, with a bound on the error of their scores (u = 6e-8).  The fast exponential is
-    // off by (4 + |x|) u relative, the reciprocal by 2 u.  sigmoid: (8 + |z|) u s.  softmax: the
-    // difference z - zmax rounds by |z - zmax| u, and the denominator (37 additions) is the same
-    // for all keys of the token: (50 + 2 |z - zmax|) u s.  Scores under 2e-38 count as that or 0.
+    // Order keys, with a bound on the error of their scores (u = 2^-24).  The fast exponential of x
+    // is off by 2 + 1.173 |x| ulp, (4 + 2.35 |x|) u relative; the reciprocal by 2 u.  sigmoid: with the
+    // addition (7 + 2.35 (1 - s) |z|) u s.  softmax: z - zmax rounds by |z - zmax| u; the sum of the
+    // exponentials has 36 additions and their mean error, |z - zmax| being ln E in the mean at most:
+    // (73 + 3.35 |z - zmax|) u s.  With R the largest score there may be (1, or the softmax of
+    // zmax), no score of at most S has an error of more than
+    //   (A + 3.35 max(1, ln(R / S))) u S,  A = 7 or 73:
+    // s |z - zmax| = s ln(R / s), and s |z| <= s ln(1 / s) for z < 0, rise with s up to R / e and stay
+    // below 0.37 R; s (1 - s) z is below 0.23 for z > 0.
+    // Scores under 2e-38 count as that or 0.
+    constexpr float kErr = SIGMOID ? 7.0f : 73.0f;
+    constexpr float kU = 6.0e-8f;  // a little above u
     uint32_t key[VPL];
     float rden = 1.0f;  // softmax: the largest score
     if (plain) {
@@ -355,12 +371,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
     }
     bool sure = true;
     if (G > 1) {
-      // value of each group, as order bits in lane g: the sum of the group's two largest keys
-      uint32_t value = 0u;
-      auto value_of = [](uint32_t a1, uint32_t a2) {
-        const float v = order_value(a1);  // -inf: no expert left in the group
-        return order_bits(a2 > kShut ? v + order_value(a2) : v);
-      };
+      // lane g: the two largest keys of group g
+      uint32_t top1 = kShut, top2 = kShut;
       if (whole) {
         const int pos = lane - my_group * lpg;
         uint32_t a1 = kShut, a2 = kShut;
@@ -376,8 +388,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
             a1 = max(a1, b1);
           }
         }
-        const uint32_t v = __shfl_sync(kFull, value_of(a1, a2), lane < G ? lane * lpg : 0);
-        if (lane < G) value = v;
+        const int from = lane < G ? lane * lpg : 0;
+        a1 = __shfl_sync(kFull, a1, from);
+        a2 = __shfl_sync(kFull, a2, from);
+        if (lane < G) top1 = a1, top2 = a2;
       } else {
         for (int g = 0; g < G; ++g) {
           uint32_t a1 = kShut, a2 = kShut;
@@ -394,29 +408,33 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
             a2 = max(max(a2, b2), min(a1, b1));
             a1 = max(a1, b1);
           }
-          if (lane == g) value = value_of(a1, a2);
+          if (lane == g) top1 = a1, top2 = a2;
         }
       }
+      // the group's value is their sum (-inf: no expert left in it)
+      const float c1 = order_value(top1), c2 = top2 > kShut ? order_value(top2) : 0.0f;
+      const float value = c1 + c2;
       // the best ones, the lower of equal ones first
       unsigned kept = 0u;
-      uint32_t last = 0u;
+      uint32_t left = order_bits(value);
       for (int j = 0; j < p.keep_groups; ++j) {
-        const uint32_t top = __reduce_max_sync(kFull, value);
+        const uint32_t top = __reduce_max_sync(kFull, left);
         if (top <= kShut) break;
-        const unsigned who = __ballot_sync(kFull, value == top);
-        const int g = __ffs(who) - 1;
+        const int g = __ffs(__ballot_sync(kFull, left == top)) - 1;
         kept |= 1u << g;
-        last = top;
-        if (lane == g) value = 0u;
+        if (lane == g) left = kShut;
       }
-      const uint32_t next = __reduce_max_sync(kFull, value);
-      if (next > kShut) {  // the last kept value against the first that is not kept
-        const float in = order_value(last), out = order_value(next);
-        // four scores of at most 1 (rden) each; |x| e^-|x| is below 0.4
-        const float tol = (SIGMOID ? 4e-6f : 1.5e-5f * rden) +
-                          5e-7f * fmaxf(fabsf(in), fabsf(out)) + 1e-36f;
-        sure = in - out > tol;
-      }
+      // Sure if the kept values, less their errors, are above the others and theirs: two scores, the
+      // rounding of their keys and that of the sum.
+      const float R = SIGMOID ? 1.0f : rden;
+      // (A NaN of a sum that overflows counts as not sure.)
+      const float err = 2.0f * (kErr + 3.5f) * kU * R + 4.0f * kU * (fabsf(c1) + fabsf(c2)) + 1e-36f;
+      const bool in = (kept >> lane) & 1u, out = !in && top1 > kShut;
+      const float least = in ? fmaxf(value - err, -INFINITY) : INFINITY;
+      const float most = out ? fminf(value + err, INFINITY) : -INFINITY;
+      const uint32_t low = __reduce_min_sync(kFull, order_bits(least));
+      const uint32_t high = __reduce_max_sync(kFull, order_bits(most));
+      sure = low > high;
       if (whole) {
         if (!((kept >> my_group) & 1u)) {
 #pragma unroll
@@ -435,25 +453,33 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
     }
     int mine = -1;             // expert of slot `lane`
     uint32_t mine_key = kShut; // its key (lane k: the best one left)
-    if (k == 32 || !topk_by_threshold<VPL>(key, k, lane, boxes[warp], mine, mine_key))
-      topk_by_rounds<VPL>(key, k, lane, mine, mine_key);
+    bool whole_order;  // no expert behind those of the lanes
+    if (k == 32 || !topk_by_threshold<VPL>(key, k, lane, boxes[warp], mine, mine_key, whole_order))
+      topk_by_rounds<VPL>(key, k, lane, mine, mine_key, whole_order);
     float zj = mine >= 0 ? load_logit<DT>(p.logits, row + mine) : -INFINITY;
     if (p.bias != nullptr) {
-      // neighbours of the order that fp32 cannot tell apart
+      // Is the order of the slots, and of the best expert left, sure?  Lane i compares expert i of
+      // the order with all behind it.  Their keys are at most that of i + 1, so none of their scores
+      // is above S.  (Rounding the sums s + b keeps their order: only the neighbours' own counts.)
       const float c = mine >= 0 ? order_value(mine_key) : 0.0f;
       const float b = mine >= 0 ? __ldg(p.bias + mine) : 0.0f;
-      const float s = fabsf(c - b) + 1.2e-7f * fabsf(c);  // the score, up to rounding
       const float c2 = __shfl_down_sync(kFull, c, 1), b2 = __shfl_down_sync(kFull, b, 1);
-      const float s2 = __shfl_down_sync(kFull, s, 1), z2 = __shfl_down_sync(kFull, zj, 1);
+      const float z2 = __shfl_down_sync(kFull, zj, 1);
       const int m2 = __shfl_down_sync(kFull, mine, 1);
-      if (lane < k && mine >= 0 && lane < 31 && m2 >= 0) {
-        const float x = SIGMOID ? fmaxf(fabsf(zj), fabsf(z2)) : zmax - fminf(zj, z2);
-        const float rel = SIGMOID ? 1.5e-6f + 1.3e-7f * x : 7e-6f + 2.6e-7f * x;
-        const float tol = rel * fmaxf(s, s2) + 2.5e-7f * fmaxf(fabsf(c), fabsf(c2)) + 1e-36f;
-        if (c - c2 <= tol && !(zj == z2 && b == b2)) sure = false;
-      }
-      if (lane == 31 && k == 32) sure = false;  // its neighbour has no lane: decide in fp64
-      sure = __all_sync(kFull, sure);
+      const bool pair = lane < 31 && mine >= 0 && m2 >= 0;
+      const float R = SIGMOID ? 1.0f : rden;
+      const float S = fmaxf(1e-36f, fminf(R, fmaxf(c - b, c2 - low_bias) +
+                                                 2.0f * kU * (fabsf(c) + fabsf(c2) + fabsf(low_bias))));
+      const float tol = 2.0f * kU * S * (kErr + 3.5f * fmaxf(1.0f, __logf(R / S))) +
+                        2.0f * kU * (fabsf(c) + fabsf(c2)) + 1e-36f;
+      const bool same = pair && zj == z2 && b == b2;
+      const unsigned close = __ballot_sync(kFull, pair && !same && !(c - c2 > tol));
+      // Equal experts are in their order already, and what is behind the second is behind the
+      // first: the last comparison that counts is the first of unequal ones from slot k - 1 on.
+      const unsigned equal = __ballot_sync(kFull, same) >> (k - 1);
+      const int last = k - 1 + __ffs(~equal) - 1;
+      const bool compared = (__ballot_sync(kFull, pair) >> last) & 1u;
+      sure = sure && !(close & (0xffffffffu >> (31 - last))) && (compared || whole_order);
     }
     if (!sure) {  // uniform across the warp
       double* kd = keys64 + (size_t)warp * E;

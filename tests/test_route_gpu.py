@@ -106,6 +106,56 @@ def test_route_large_bias_hides_the_scores_from_fp32():
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_a_coarse_key_below_a_fine_pair(kind):
+    """Two experts of small scores, 8e-9 apart and told apart by fp32, above one of a large score and a
+    negative bias whose key is within 6e-8 of theirs: only 64 bits say whether it is first."""
+    T, E = 500, 6
+    z = torch.full((T, E), -20.0, dtype=torch.float64)
+    z[:, 0] = 0.0
+    z[:, 1] = -7.0
+    z[:, 4] = 4e-3
+    s = torch.from_numpy(R.scores(z[0].numpy(), kind))
+    z[:, 3] = -7.0 - 8e-9 / float(s[1])                                  # ds = s dz
+    z[:, 4] += torch.linspace(-1, 1, T, dtype=torch.float64) * 6e-8 * 4  # ds = dz / 4
+    for step in range(12):  # across the grid of the large score's fp32 values
+        fine = 1e-4 + step * 1e-8
+        bias = torch.tensor([-9.0, fine, 0.0, fine, 0.0, 0.0])
+        bias[4] = float(s[1]) + 1e-4 - float(s[4])
+        check(z.float(), 1, bias, kind)
+        check(z.float(), 2, bias, kind)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_route_group_of_large_keys_of_both_signs(kind):
+    """A group's value 1000 + s - 999.5 + s' is of the order of 1, its keys round by 3e-5."""
+    T, E = 2000, 8
+    g = torch.Generator().manual_seed(8)
+    z = torch.zeros(T, E, dtype=torch.float64)
+    z[:, 2:4] = z[:, 6:] = -float("inf")
+    z[:, 0] = 0.01 * torch.randn(T, generator=g)
+    bias = torch.tensor([1000.0, -999.5, 0.0, 0.0, 0.25, 0.25, 0.0, 0.0])
+    # the two groups' values differ by some 1e-5: all scores but expert 0's and 4's are the same
+    z[:, 4] = z[:, 0] + 8e-5 * torch.randn(T, generator=g, dtype=torch.float64)
+    check(z.float(), 1, bias, kind, 2, 1)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("equal", [2, 3, 12])
+@pytest.mark.parametrize("E", [40, 300])
+def test_route_near_tie_behind_equal_experts(E, equal, kind):
+    """Equal experts around the last slot, and after them one whose logit is an ulp larger but whose
+    fp32 score is the same."""
+    z = torch.full((4, E), -1.0)
+    z += torch.linspace(0, 0.5, E)
+    z[:, 5] = 4.0
+    z[:, 6:6 + equal] = 3.0
+    z[:, 6 + equal] = 3.0 + 2.0 ** -22
+    bias = torch.zeros(E)
+    for k in (1, 2, 3):
+        check(z, k, bias, kind)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("G", [1, 4])
 def test_route_masks(kind, dt, G):
