@@ -16,10 +16,12 @@
 // One warp per token.  Expert e = lane * VPL + i lives in register i of a lane, so the lowest
 // lane that holds a maximum holds the lowest expert.
 //
-// Bound by the instructions issued (60-70% of the issue slots; the bytes would take 1-2 us): T =
-// 16384, E = 128, top-8: 12 us (470 instructions a token); T = 16383, E = 256 in 8 groups, bias,
-// sigmoid: 31 us (920).  One token: a launch.  Gradient, T = 16384, E = 128, top-8, renormalised: 7.7
-// us, latency and the 8.4 MB of the result; softmax of 160 experts, not renormalised, T = 8191: 10 us.
+// Bound by the latency and the number of a token's dependent steps (67-70% of the issue slots; the
+// bytes would take 1-2 us): T = 16384, E = 128, top-8: 9 us (440 instructions a token), with a bias,
+// sigmoid: 13 us (670); T = 16383, E = 256 in 8 groups, bias, sigmoid: 23 us (1040).  A token that goes
+// to fp64 takes 0.6 us more for the order of its slots, 3 us for its groups, 6 for all keys.  One
+// token: a launch.  Gradient, T = 16384, E = 128, top-8, renormalised: 7.7 us, latency and the 8.4 MB of
+// the result; softmax of 160 experts, not renormalised, T = 8191: 10 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -140,58 +142,118 @@ __device__ __forceinline__ void merge_top2(F& a1, F& a2, F b1, F b2) {
   }
 }
 
+// Order-preserving bits of a double that is not NaN, and those of -inf (see order_bits).
+__device__ __forceinline__ uint64_t order_bits64(double d) {
+  const long long b = __double_as_longlong(d + 0.0);
+  return (uint64_t)b ^ ((uint64_t)(b >> 63) | 0x8000000000000000ull);
+}
+constexpr uint64_t kShut64 = 0x000fffffffffffffull;
+
 // fp64 selection over the keys key[0..E) of one token (shared memory, -inf: not to be chosen);
-// one warp.  keep_groups_fp64 closes the experts of the groups that do not stay;
-// topk_fp64 returns the expert of slot `lane` (-1: none left).
-__device__ __noinline__ void keep_groups_fp64(double* key, int E, int G, int keep, int lane) {
-  const double kNone = -INFINITY;
-  const int n = E / G;
-  double value = kNone;  // of group `lane`
-  for (int g = 0; g < G; ++g) {
-    double a1 = kNone, a2 = kNone;
-    for (int i = lane; i < n; i += 32) merge_top2(a1, a2, key[g * n + i], kNone);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const double b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
-      merge_top2(a1, a2, b1, b2);
-    }
-    if (lane == g && a1 > kNone) value = a2 > kNone ? a1 + a2 : a1;
+// one warp.  order_fp64 orders the experts of lanes 0 .. n - 1 and returns that of this lane's place.
+// keys_fp64 computes all keys; kept_groups_fp64 returns the groups that stay, `sub`
+// neighbouring lanes to a group; topk_fp64 returns the expert of slot `lane` (-1:
+// none left).  Few tokens come here, so what counts is how long one takes, from cold instructions
+// on, since the end of the launch waits for it: short loops.
+template <lrmoe_dtype DT>
+__device__ __noinline__ double sum_fp64(const void* logits, int E, size_t row, float zmax, int lane) {
+  double sum = 0.0;  // the softmax's denominator
+#pragma unroll 4
+  for (int e = lane; e < E; e += 32) {
+    const float z = load_logit<DT>(logits, row + e);
+    if (z > -INFINITY && z < INFINITY) sum += exp((double)z - (double)zmax);
   }
+  return warp_sum(sum);
+}
+
+template <lrmoe_dtype DT, bool SIGMOID>
+__device__ __noinline__ void keys_fp64(const void* logits, const float* bias, int E, size_t row,
+                                       float zmax, double* key, int lane) {
+  const double inv = SIGMOID ? 1.0 : 1.0 / sum_fp64<DT>(logits, E, row, zmax, lane);
+  __syncwarp();
+#pragma unroll 4
+  for (int e = lane; e < E; e += 32) {
+    const float z = load_logit<DT>(logits, row + e), b = bias != nullptr ? __ldg(bias + e) : 0.0f;
+    double s = exp(SIGMOID ? -(double)z : (double)z - (double)zmax);
+    s = SIGMOID ? 1.0 / (1.0 + s) : s * inv;
+    const bool open = z > -INFINITY && z < INFINITY && b > -INFINITY && b < INFINITY;
+    key[e] = open ? s + (double)b : -INFINITY;
+  }
+  __syncwarp();
+}
+
+template <lrmoe_dtype DT, bool SIGMOID>
+__device__ __noinline__ int order_fp64(const void* logits, int E, size_t row, float zmax, int mine,
+                                       float z, float b, int n, uint64_t* box, int lane) {
+  const double inv = SIGMOID ? 1.0 : 1.0 / sum_fp64<DT>(logits, E, row, zmax, lane);
+  double v = exp(SIGMOID ? -(double)z : (double)z - (double)zmax);
+  v = (SIGMOID ? 1.0 / (1.0 + v) : v * inv) + (double)b;
   int rank = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const double ov = __shfl_sync(kFull, v, i);
+    const int om = __shfl_sync(kFull, mine, i);
+    rank += ov > v || (ov == v && om < mine) ? 1 : 0;
+  }
+  if (lane < n) box[rank] = (uint64_t)mine;
+  __syncwarp();
+  if (lane < n) mine = (int)box[lane];
+  __syncwarp();
+  return mine;
+}
+
+__device__ __noinline__ unsigned kept_groups_fp64(const double* key, int E, int G, int keep, int lane) {
+  const double kNone = -INFINITY;
+  const int n = E / G, sub = 1 << (31 - __clz(32 / G)), mine = lane / sub;
+  double a1 = kNone, a2 = kNone;
+  if (mine < G) {
+#pragma unroll 4
+    for (int i = lane % sub; i < n; i += sub) merge_top2(a1, a2, key[mine * n + i], kNone);
+  }
+  for (int o = 1; o < sub; o <<= 1) {
+    const double b1 = __shfl_xor_sync(kFull, a1, o), b2 = __shfl_xor_sync(kFull, a2, o);
+    merge_top2(a1, a2, b1, b2);
+  }
+  double value = a2 > kNone ? a1 + a2 : a1;  // of group `lane`
+  value = __shfl_sync(kFull, value, (lane * sub) & 31);
+  if (lane >= G) value = kNone;
+  int rank = 0;
+#pragma unroll 4
   for (int g = 0; g < G; ++g) {
     const double v = __shfl_sync(kFull, value, g);
     rank += (v > value || (v == value && g < lane)) ? 1 : 0;
   }
-  const unsigned kept = __ballot_sync(kFull, lane < G && rank < keep && value > kNone);
-  __syncwarp();
-  for (int e = lane; e < E; e += 32)
-    if (!((kept >> (e / n)) & 1u)) key[e] = kNone;
-  __syncwarp();
+  return __ballot_sync(kFull, rank < keep && value > kNone);
 }
 
 __device__ __noinline__ int topk_fp64(double* key, int E, int k, int lane) {
-  const double kNone = -INFINITY;
-  int mine = -1;
-  for (int j = 0; j < k; ++j) {
-    double best = kNone;
-    int at = E;
-    for (int e = lane; e < E; e += 32)
-      if (key[e] > best) {
-        best = key[e];
+  uint64_t best;  // of this lane's experts: lane, lane + 32, ...
+  int at;
+  auto scan = [&] {
+    best = kShut64;
+    at = E;
+    for (int e = lane; e < E; e += 32) {
+      const uint64_t v = order_bits64(key[e]);
+      if (v > best) {
+        best = v;
         at = e;
       }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const double ob = __shfl_xor_sync(kFull, best, o);
-      const int oa = __shfl_xor_sync(kFull, at, o);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
     }
-    if (!(best > kNone)) break;  // uniform: nothing left
-    if (lane == j) mine = at;
-    if (lane == 0) key[at] = kNone;
+  };
+  scan();
+  int mine = -1;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t high = __reduce_max_sync(kFull, (uint32_t)(best >> 32));
+    bool top = (uint32_t)(best >> 32) == high;
+    const uint32_t low = __reduce_max_sync(kFull, top ? (uint32_t)best : 0u);
+    if ((((uint64_t)high << 32) | low) <= kShut64) break;  // uniform: nothing left
+    top = top && (uint32_t)best == low;
+    const int first = (int)__reduce_min_sync(kFull, top ? (unsigned)at : (unsigned)E);
+    if (lane == j) mine = first;
+    if (top && at == first) {
+      key[at] = -INFINITY;
+      scan();
+    }
     __syncwarp();
   }
   return mine;
@@ -286,13 +348,14 @@ __device__ __noinline__ void topk_by_rounds(uint32_t (&key)[VPL], int k, int lan
   }
 }
 
-template <lrmoe_dtype DT, bool SIGMOID, int VPL>
-__global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 : 1) route_kernel(const RouteParams p) {
+// PLAIN: no bias and no groups, so that the order is that of the logits.
+template <lrmoe_dtype DT, bool SIGMOID, bool PLAIN, int VPL>
+__global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 : VPL == 16 ? 4 : 2) route_kernel(const RouteParams p) {
   extern __shared__ double keys64[];  // [kRouteWarps][E], when a bias or groups are given
   __shared__ __align__(16) uint64_t boxes[kRouteWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int E = p.E, k = p.k, G = p.groups;
-  const bool plain = p.bias == nullptr && G == 1;  // the order is that of the logits
+  const int E = p.E, k = p.k, G = PLAIN ? 1 : p.groups;
+  const float* biases = PLAIN ? nullptr : p.bias;
   const int e0 = lane * VPL;
   const int n = p.n;
   // groups of whole lanes: a lane's experts belong to one group, a group to lpg neighbouring lanes
@@ -306,14 +369,14 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
   float low_bias = INFINITY;  // the lowest finite one
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    bias[i] = p.bias != nullptr && e0 + i < E ? __ldg(p.bias + e0 + i) : 0.0f;
+    bias[i] = biases != nullptr && e0 + i < E ? __ldg(biases + e0 + i) : 0.0f;
     if (!(bias[i] < INFINITY)) {
       bad_bias = true;
       bias[i] = -INFINITY;
     }
     if (e0 + i < E && bias[i] > -INFINITY) low_bias = fminf(low_bias, bias[i]);
   }
-  if (p.bias != nullptr) low_bias = -warp_max(-low_bias);
+  if (biases != nullptr) low_bias = -warp_max(-low_bias);
   // 64-bit: T may be near 2^31
   for (long long t = (long long)blockIdx.x * kRouteWarps + warp; t < p.T;
        t += (long long)gridDim.x * kRouteWarps) {
@@ -331,7 +394,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       if (!SIGMOID) zmax = fmaxf(zmax, z[i]);
     }
     if (__any_sync(kFull, bad) && lane == 0) raise_status(p.status, LRMOE_ST_NONFINITE);
-    if (!SIGMOID && !(plain && p.renorm)) zmax = warp_max(zmax);
+    if (!SIGMOID && !(PLAIN && p.renorm)) zmax = warp_max(zmax);
     // Order keys, with a bound on the error of their scores (u = 2^-24).  The fast exponential of x
     // is off by 2 + 1.173 |x| ulp, (4 + 2.35 |x|) u relative; the reciprocal by 2 u.  sigmoid: with the
     // addition (7 + 2.35 (1 - s) |z|) u s.  softmax: z - zmax rounds by |z - zmax| u; the sum of the
@@ -346,7 +409,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
     constexpr float kU = 6.0e-8f;  // a little above u
     uint32_t key[VPL];
     float rden = 1.0f;  // softmax: the largest score
-    if (plain) {
+    if constexpr (PLAIN) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = order_bits(z[i]);
     } else {
@@ -369,7 +432,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       for (int i = 0; i < VPL; ++i)
         key[i] = order_bits(z[i] > -INFINITY ? sc[i] + bias[i] : -INFINITY);
     }
-    bool sure = true;
+    double* kd = keys64 + (size_t)warp * E;
+    unsigned kept = 0u;  // groups
     if (G > 1) {
       // lane g: the two largest keys of group g
       uint32_t top1 = kShut, top2 = kShut;
@@ -415,7 +479,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       const float c1 = order_value(top1), c2 = top2 > kShut ? order_value(top2) : 0.0f;
       const float value = c1 + c2;
       // the best ones, the lower of equal ones first
-      unsigned kept = 0u;
       uint32_t left = order_bits(value);
       for (int j = 0; j < p.keep_groups; ++j) {
         const uint32_t top = __reduce_max_sync(kFull, left);
@@ -434,7 +497,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
       const float most = out ? fminf(value + err, INFINITY) : -INFINITY;
       const uint32_t low = __reduce_min_sync(kFull, order_bits(least));
       const uint32_t high = __reduce_max_sync(kFull, order_bits(most));
-      sure = low > high;
+      if (low <= high) {
+        keys_fp64<DT, SIGMOID>(p.logits, biases, E, row, zmax, kd, lane);
+        kept = kept_groups_fp64(kd, E, G, p.keep_groups, lane);
+      }
       if (whole) {
         if (!((kept >> my_group) & 1u)) {
 #pragma unroll
@@ -445,7 +511,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
         for (int i = 0; i < VPL; ++i)
           if (e0 + i < E && !((kept >> ((e0 + i) / n)) & 1u)) key[i] = kShut;
       }
-      if (p.bias == nullptr) {  // inside the kept groups the score rises with the logit
+      if (biases == nullptr) {  // inside the kept groups the score rises with the logit
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
           if (key[i] != kShut) key[i] = order_bits(z[i]);
@@ -457,63 +523,52 @@ __global__ void __launch_bounds__(32 * kRouteWarps, VPL <= 4 ? 8 : VPL == 8 ? 6 
     if (k == 32 || !topk_by_threshold<VPL>(key, k, lane, boxes[warp], mine, mine_key, whole_order))
       topk_by_rounds<VPL>(key, k, lane, mine, mine_key, whole_order);
     float zj = mine >= 0 ? load_logit<DT>(p.logits, row + mine) : -INFINITY;
-    if (p.bias != nullptr) {
+    if (biases != nullptr) {
       // Is the order of the slots, and of the best expert left, sure?  Lane i compares expert i of
-      // the order with all behind it.  Their keys are at most that of i + 1, so none of their scores
-      // is above S.  (Rounding the sums s + b keeps their order: only the neighbours' own counts.)
+      // the order with all behind it.  Their keys are at most c2, that of i + 1, so none of their
+      // scores is above S.  (Rounding the sums s + b keeps their order: only the rounding of c
+      // and c2 counts.)
       const float c = mine >= 0 ? order_value(mine_key) : 0.0f;
-      const float b = mine >= 0 ? __ldg(p.bias + mine) : 0.0f;
+      const float b = mine >= 0 ? __ldg(biases + mine) : 0.0f;
+      const float R = SIGMOID ? 1.0f : rden;
+      auto above = [&](float c2) {
+        const float S = fmaxf(1e-36f, fminf(R, fmaxf(c - b, c2 - low_bias) +
+                                                   2.0f * kU * (fabsf(c) + fabsf(c2) + fabsf(low_bias))));
+        return c - c2 > 2.0f * kU * S * (kErr + 3.5f * fmaxf(1.0f, __logf(R / S))) +
+                            2.0f * kU * (fabsf(c) + fabsf(c2)) + 1e-36f;
+      };
       const float c2 = __shfl_down_sync(kFull, c, 1), b2 = __shfl_down_sync(kFull, b, 1);
       const float z2 = __shfl_down_sync(kFull, zj, 1);
-      const int m2 = __shfl_down_sync(kFull, mine, 1);
-      const bool pair = lane < 31 && mine >= 0 && m2 >= 0;
-      const float R = SIGMOID ? 1.0f : rden;
-      const float S = fmaxf(1e-36f, fminf(R, fmaxf(c - b, c2 - low_bias) +
-                                                 2.0f * kU * (fabsf(c) + fabsf(c2) + fabsf(low_bias))));
-      const float tol = 2.0f * kU * S * (kErr + 3.5f * fmaxf(1.0f, __logf(R / S))) +
-                        2.0f * kU * (fabsf(c) + fabsf(c2)) + 1e-36f;
+      const unsigned have = __ballot_sync(kFull, mine >= 0);
+      const bool pair = (have >> 1 >> lane) & 1u;  // lanes 0 .. n - 1 have an expert
       const bool same = pair && zj == z2 && b == b2;
-      const unsigned close = __ballot_sync(kFull, pair && !same && !(c - c2 > tol));
+      const unsigned close = __ballot_sync(kFull, pair && !same && !above(c2));
       // Equal experts are in their order already, and what is behind the second is behind the
       // first: the last comparison that counts is the first of unequal ones from slot k - 1 on.
       const unsigned equal = __ballot_sync(kFull, same) >> (k - 1);
       const int last = k - 1 + __ffs(~equal) - 1;
-      const bool compared = (__ballot_sync(kFull, pair) >> last) & 1u;
-      sure = sure && !(close & (0xffffffffu >> (31 - last))) && (compared || whole_order);
-    }
-    if (!sure) {  // uniform across the warp
-      double* kd = keys64 + (size_t)warp * E;
-      double den64 = 1.0;
-      if constexpr (!SIGMOID) {
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (z[i] > -INFINITY) sum += exp((double)z[i] - (double)zmax);
-        den64 = warp_sum(sum);
-      }
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (e0 + i >= E) continue;
-        double c = -INFINITY;
-        const float b = bias[i];
-        if (z[i] > -INFINITY && b > -INFINITY) {
-          c = SIGMOID ? 1.0 / (1.0 + exp(-(double)z[i]))
-                      : exp((double)z[i] - (double)zmax) / den64;
-          c += (double)b;
+      const bool compared = (have >> 1 >> last) & 1u;
+      bool sure = !(close & (0xffffffffu >> (31 - last))) && (compared || whole_order);
+      if (!sure) {
+        // If the slots' experts are above all that have no lane, the fp64 keys of the lanes decide.
+        const int found = __popc(have);
+        const float lowest = __shfl_sync(kFull, c, found - 1);
+        if (whole_order || __all_sync(kFull, lane >= k || above(lowest))) {
+          mine = order_fp64<DT, SIGMOID>(p.logits, E, row, zmax, mine, zj, b, found, boxes[warp], lane);
+          zj = mine >= 0 ? load_logit<DT>(p.logits, row + mine) : -INFINITY;
+          sure = true;
         }
-        kd[e0 + i] = c;
       }
-      __syncwarp();
-      if (G > 1) keep_groups_fp64(kd, E, G, p.keep_groups, lane);
-      if (p.bias == nullptr) {  // the score rises with the logit
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (e0 + i < E && kd[e0 + i] > -INFINITY) kd[e0 + i] = (double)z[i];
-        __syncwarp();
+      if (!sure) {  // uniform across the warp
+        keys_fp64<DT, SIGMOID>(p.logits, biases, E, row, zmax, kd, lane);
+        if (G > 1) {
+          for (int e = lane; e < E; e += 32)
+            if (!((kept >> (e / n)) & 1u)) kd[e] = -INFINITY;
+          __syncwarp();
+        }
+        mine = topk_fp64(kd, E, k, lane);
+        zj = mine >= 0 ? load_logit<DT>(p.logits, row + mine) : -INFINITY;
       }
-      mine = topk_fp64(kd, E, k, lane);
-      __syncwarp();
-      zj = mine >= 0 ? load_logit<DT>(p.logits, row + mine) : -INFINITY;
     }
     // weights of the slots
     const bool slot = lane < k;
@@ -739,35 +794,42 @@ __global__ void __launch_bounds__(256) route_grad_dense_kernel(const RouteGradPa
   }
 }
 
-template <lrmoe_dtype DT, bool SIGMOID>
+template <lrmoe_dtype DT, bool SIGMOID, bool PLAIN>
 cudaError_t route_by_width(RouteParams p, cudaStream_t s) {
-  auto kern = route_kernel<DT, SIGMOID, 32>;
+  auto kern = route_kernel<DT, SIGMOID, PLAIN, 32>;
   int vpl = 32;  // experts of a lane
   if (p.E <= 32) {
-    kern = route_kernel<DT, SIGMOID, 1>;
+    kern = route_kernel<DT, SIGMOID, PLAIN, 1>;
     vpl = 1;
   } else if (p.E <= 64) {
-    kern = route_kernel<DT, SIGMOID, 2>;
+    kern = route_kernel<DT, SIGMOID, PLAIN, 2>;
     vpl = 2;
   } else if (p.E <= 128) {
-    kern = route_kernel<DT, SIGMOID, 4>;
+    kern = route_kernel<DT, SIGMOID, PLAIN, 4>;
     vpl = 4;
   } else if (p.E <= 256) {
-    kern = route_kernel<DT, SIGMOID, 8>;
+    kern = route_kernel<DT, SIGMOID, PLAIN, 8>;
     vpl = 8;
   } else if (p.E <= 512) {
-    kern = route_kernel<DT, SIGMOID, 16>;
+    kern = route_kernel<DT, SIGMOID, PLAIN, 16>;
     vpl = 16;
   }
   p.n = p.E / p.groups;
   p.lpg = p.n % vpl == 0 ? p.n / vpl : 0;
-  const bool plain = p.bias == nullptr && p.groups == 1;
-  const size_t smem = plain ? 0 : sizeof(double) * (size_t)kRouteWarps * p.E;  // <= 32 KB
+  const size_t smem = PLAIN ? 0 : sizeof(double) * (size_t)kRouteWarps * p.E;  // <= 32 KB
   long long blocks = ((long long)p.T + kRouteWarps - 1) / kRouteWarps;
-  // about what is resident at once: a warp keeps its biases over several tokens
-  const long long cap = (long long)num_sms() * (p.E <= 256 ? 8 : 4);
+  // A warp keeps its biases over several tokens.  Tokens take unequal times (those that go to
+  // fp64 and back 1.5 times as long and more), so more blocks than are resident at once: E = 256 in
+  // groups, T = 16383, 16 to an SM 22.8 us, 8 to an SM 26; with wider rows the biases count for more.
+  const long long cap = (long long)num_sms() * (p.E <= 256 ? 16 : 4);
   if (blocks > cap) blocks = cap;
   return launch_pdl(kern, dim3((unsigned)blocks), dim3(32 * kRouteWarps), smem, s, p);
+}
+
+template <lrmoe_dtype DT, bool SIGMOID>
+cudaError_t route_by_order(const RouteParams& p, cudaStream_t s) {
+  return p.bias == nullptr && p.groups == 1 ? route_by_width<DT, SIGMOID, true>(p, s)
+                                            : route_by_width<DT, SIGMOID, false>(p, s);
 }
 
 template <lrmoe_dtype DT, bool SIGMOID, bool RENORM>
@@ -821,8 +883,8 @@ cudaError_t launch_route(const void* logits, int T, int E, lrmoe_dtype dt, const
   const RouteParams p{logits, bias, T, E, k, n_group, topk_group, renorm, 0, 0, scale, idx, w, status};
   const bool sg = fn == LRMOE_SCORE_SIGMOID;
   if (dt == LRMOE_BF16)
-    return sg ? route_by_width<LRMOE_BF16, true>(p, s) : route_by_width<LRMOE_BF16, false>(p, s);
-  return sg ? route_by_width<LRMOE_F32, true>(p, s) : route_by_width<LRMOE_F32, false>(p, s);
+    return sg ? route_by_order<LRMOE_BF16, true>(p, s) : route_by_order<LRMOE_BF16, false>(p, s);
+  return sg ? route_by_order<LRMOE_F32, true>(p, s) : route_by_order<LRMOE_F32, false>(p, s);
 }
 
 cudaError_t launch_route_grad(const void* logits, int T, int E, lrmoe_dtype dt, const int32_t* idx,

@@ -200,6 +200,29 @@ def test_route_many_tokens_and_repeat():
     np.testing.assert_array_equal(a[0], want.numpy())
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,keep", [(256, 8, 8, 4), (128, 8, 1, 1), (160, 6, 8, 3), (32, 31, 1, 1), (512, 10, 1, 1),
+                                        (40, 32, 1, 1)])
+def test_route_selects_by_64_bits_among_many_tokens(E, k, G, keep, kind):
+    """20000 tokens of each scale of logits and biases: some come as near as fp32 cannot tell."""
+    g = torch.Generator("cuda").manual_seed(E + k)
+    for sigma in (0.01, 1.0, 6.0):
+        for size in (None, 0.0, 0.02, 1.0, 1e4):
+            z = torch.randn(20000, E, generator=g, device="cuda") * sigma
+            bias = None if size is None else torch.randn(E, generator=g, device="cuda") * size
+            d = z.double()
+            key = 1 / (1 + torch.exp(-d)) if kind == "sigmoid" else torch.softmax(d, 1)
+            key = key + (0 if bias is None else bias.double())
+            value = key.view(-1, G, E // G).topk(min(2, E // G), 2).values.sum(2)
+            kept = torch.zeros_like(value, dtype=torch.bool)
+            kept.scatter_(1, value.sort(dim=1, descending=True, stable=True).indices[:, :keep], True)
+            order = (d if bias is None else key).masked_fill(~kept.repeat_interleave(E // G, 1), -float("inf"))
+            want = order.sort(dim=1, descending=True, stable=True).indices[:, :k].int().cpu().numpy()
+            got, _, st = run(z, k, bias, kind, n_group=G, topk_group=keep)
+            np.testing.assert_array_equal(got, want)
+            assert st == 0
+
+
 def test_route_offsets_past_32_bits():
     """More than 2^31 logits: the last tokens read and write the right rows."""
     T, E, k = 4194310, 513, 2
