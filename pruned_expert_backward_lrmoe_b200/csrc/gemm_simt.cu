@@ -189,12 +189,8 @@ struct FpropF32 {
 
 // 128 CUDA-core multiply-adds a cycle and SM are the limit for large layers; the layers that fp32
 // is for are small, and there the latency of a tile is: T = 1021, K = 256, N = 512, one expert,
-// residual: 16 us.
+// residual: 14 us.
 //
-// Ring of FS 16-deep K slices, copied asynchronously as they lie in memory; rows of 20 floats keep
-// the 16-byte reads of neighbouring columns in different banks.
-constexpr int FS = 4, FP = BK + 4;
-
 // Two fp32 multiply-adds in one instruction, each rounded as fmaf.
 __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
@@ -205,28 +201,40 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
 // 8 x 4 takes 125).
 constexpr int RI = 8;
 constexpr int TY = BM / RI;   // thread rows
-constexpr int FT = 16 * TY;   // threads
+constexpr int FT = 16 * TY;   // threads of a K group
 constexpr int LR = FT / 4;    // tile rows that the threads load in a pass
 
-template <int TN>
-__global__ void __launch_bounds__(FT) fprop_simt_kernel(const FpropF32 p) {
+// Ring of FS slices of K, copied asynchronously as they lie in memory; rows padded by four
+// floats keep the 16-byte reads of neighbouring columns in different banks.  KS groups of FT threads
+// take 16 of a slice's k each and add up at the end.
+template <int TN, int KS>
+struct FpropRing {
+  static constexpr int D = BK * KS, P = D + 4, FS = 4;
+  float A[FS][BM][P];
+  float B[FS][TN][P];
+};
+
+template <int TN, int KS>
+__global__ void __launch_bounds__(KS * FT) fprop_simt_kernel(const FpropF32 p) {
   constexpr int CJ = TN / 16;  // columns of a thread
   constexpr int AL = BM / LR, BL = TN > LR ? TN / LR : 1;
+  using Ring = FpropRing<TN, KS>;
+  constexpr int D = Ring::D, FS = Ring::FS;
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  auto& As = reinterpret_cast<Ring*>(dynamic)->A;
+  auto& Bs = reinterpret_cast<Ring*>(dynamic)->B;
   __shared__ int tstart[kMaxExperts + 1];
   __shared__ int scratch[33];
-  __shared__ __align__(16) float As[FS][BM][FP];
-  __shared__ __align__(16) float Bs[FS][TN][FP];
   __shared__ int src[BM];   // source row of each tile row (-1: none)
   __shared__ int dest[BM];  // output row of each tile row (-1: none)
   pdl_wait();
-  pdl_trigger();
   const int E = p.E, K = p.K, N = p.N;
   const int feat = p.swiglu ? TN / 2 : TN;
   const int n_tiles = (N + feat - 1) / feat;
   const int total = offsets_invalid(p.offsets, E, p.rows_cap, p.status)
                         ? 0 : build_dgrad_tiles(p.offsets, E, BM, n_tiles, tstart, scratch);
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int lr = tid >> 2, lk = (tid & 3) * 4;  // tile row and first k of this thread's loads
+  const int tid = threadIdx.x, group = tid / FT, part = tid % FT, tx = part & 15, ty = part >> 4;
+  const int lr = tid / (D / 4), lk = tid % (D / 4) * 4;  // tile row and first k of its loads
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
     const int e = find_group(tstart, E, t);
     const int local = t - tstart[e];
@@ -269,9 +277,11 @@ __global__ void __launch_bounds__(FT) fprop_simt_kernel(const FpropF32 p) {
       wp[i] = ok ? p.W + ((size_t)e * (p.swiglu ? 2 * N : N) + w) * K : nullptr;
     }
     uint64_t acc2[RI][CJ] = {};  // sums over even k (low word) and odd k (high word)
-    const int steps = (K + BK - 1) / BK;
+    const int steps = (K + D - 1) / D;
+    int in = 0, f = 0;  // slices of the ring to fill and to read
     auto fetch = [&](int step) {  // this thread's 16-byte pieces of a slice (K % 4 == 0)
-      const int k = step * BK + lk, f = step % FS;
+      const int k = step * D + lk, f = in;
+      in = in + 1 == FS ? 0 : in + 1;
       if (step < steps) {
 #pragma unroll
         for (int i = 0; i < AL; ++i) {
@@ -289,13 +299,14 @@ __global__ void __launch_bounds__(FT) fprop_simt_kernel(const FpropF32 p) {
     };
 #pragma unroll
     for (int i = 0; i < FS - 1; ++i) fetch(i);
+#pragma unroll 1
     for (int step = 0; step < steps; ++step) {
       cp_async_wait_group<FS - 2>();
       __syncthreads();  // slice `step` is there for every thread, slice step - 1 is read
       fetch(step + FS - 1);
-      const int f = step % FS;
 #pragma unroll
-      for (int kk = 0; kk < BK; kk += 4) {
+      for (int kk0 = 0; kk0 < BK; kk0 += 4) {
+        const int kk = group * BK + kk0;
         ulonglong2 av[RI], bv[CJ];  // (k, k + 1), (k + 2, k + 3)
 #pragma unroll
         for (int i = 0; i < RI; ++i)
@@ -312,6 +323,7 @@ __global__ void __launch_bounds__(FT) fprop_simt_kernel(const FpropF32 p) {
 #pragma unroll
           for (int j = 0; j < CJ; ++j) fma2(acc2[i][j], av[i].y, bv[j].y);
       }
+      f = f + 1 == FS ? 0 : f + 1;
     }
     float acc[RI][CJ];
 #pragma unroll
@@ -319,10 +331,30 @@ __global__ void __launch_bounds__(FT) fprop_simt_kernel(const FpropF32 p) {
 #pragma unroll
       for (int j = 0; j < CJ; ++j)
         acc[i][j] = __uint_as_float((uint32_t)acc2[i][j]) + __uint_as_float((uint32_t)(acc2[i][j] >> 32));
+    if constexpr (KS == 2) {  // each group finishes half of the thread's rows
+      __syncthreads();        // the ring has been read
+      float* swap = &As[0][0][0];
+      static_assert(RI / 2 * CJ * 2 * FT <= FS * BM * Ring::P, "the sums fit into the ring");
+#pragma unroll
+      for (int i = 0; i < RI / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j)
+          swap[((group * RI / 2 + i) * CJ + j) * FT + part] = group ? acc[i][j] : acc[i + RI / 2][j];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < RI / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < CJ; ++j)
+          acc[i][j] = (group ? acc[i + RI / 2][j] : acc[i][j]) +
+                      swap[(((group ^ 1) * RI / 2 + i) * CJ + j) * FT + part];
+    }
+    // Not earlier: blocks of the next launch that move in during a launch of fewer tiles than SMs hold
+    // crowd some SMs (128 tiles, back to back: 12.7 us with a trigger at the start, 11.1 here).
+    if (t + (long long)gridDim.x >= total) pdl_trigger();
     // columns tx + 16 j of the tile: SwiGLU holds gate features tx (and tx + 16) and their ups
 #pragma unroll
-    for (int i = 0; i < RI; ++i) {
-      const int m = ty + TY * i;
+    for (int i = 0; i < RI / KS; ++i) {
+      const int m = ty + TY * (i + group * RI / 2);
       const int d = dest[m];
       if (d < 0) continue;
       const size_t at = (size_t)d * N;
@@ -362,13 +394,18 @@ cudaError_t fprop_simt(const FpropF32& p, cudaStream_t s) {
     const int feat = p.swiglu ? tn / 2 : tn;
     return ((long long)p.rows_cap / BM + p.E) * ((p.N + feat - 1) / feat);
   };
-  // 64-column tiles do more products per read of shared memory, 32-column ones spread a small
-  // product over more SMs: 8192 x 512 x 512 125 and 134 us, 2048 x 256 x 256 over four experts 19.4
-  // and 16.3.
+  // 64-column tiles do more products per read of shared memory; 32-column ones with two K groups
+  // spread a small product over more SMs and warps: 8192 x 512 x 512 125 and 134 us, 2048 x 256 x 256 over
+  // four experts 19.4 and 14.5 (16.3 with one K group).
   const bool narrow = tiles(64) < 4ll * num_sms();
   const long long n = tiles(narrow ? 32 : 64), cap = 8ll * num_sms();
-  auto kern = narrow ? fprop_simt_kernel<32> : fprop_simt_kernel<64>;
-  return launch_pdl(kern, dim3((unsigned)(n < cap ? n : cap)), dim3(FT), 0, s, p);
+  auto launch = [&](auto kern, size_t ring, int threads) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kern, dim3((unsigned)(n < cap ? n : cap)), dim3(threads), ring, s, p);
+  };
+  return narrow ? launch(fprop_simt_kernel<32, 2>, sizeof(FpropRing<32, 2>), 2 * FT)
+                : launch(fprop_simt_kernel<64, 1>, sizeof(FpropRing<64, 1>), FT);
 }
 
 }  // namespace
