@@ -159,6 +159,18 @@ def test_linear_long_experts(K, N, extras):
     test_linear("long", K, N, extras, "bf16")
 
 
+@pytest.mark.parametrize("K,N", [(72, 2056), (520, 1032), (4, 4100)])
+@pytest.mark.parametrize("extras", ["plain", "all", "in place"])
+def test_linear_long_experts_f32(K, N, extras):
+    """Wide tiles, several to a block."""
+    test_linear("long", K, N, extras, "f32")
+
+
+@pytest.mark.parametrize("H,I", [(68, 1160), (136, 2188)])
+def test_swiglu_long_experts_f32(H, I):
+    test_swiglu_gathered("long", H, I, 4, True, "gua", "f32")
+
+
 @pytest.mark.parametrize("sizes", [[4096] * 4, [4097] * 4, [16500], [3, 20000, 5]])
 def test_linear_with_uneven_last_tiles(sizes):
     """No last tile at all, one in every expert, one expert that holds nearly all rows."""
