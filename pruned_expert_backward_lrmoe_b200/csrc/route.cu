@@ -675,6 +675,7 @@ __device__ __forceinline__ void store_logit(void* z, size_t i, float v) {
 //   sigmoid:      d_j = scale dw_j s_j (1 - s_j)
 // and dz_e = sum of d over the slots of e: the row is zeros but for the slots' experts, so only
 // their logits are read.  SUB lanes take a token (k <= SUB), a warp 32 / SUB neighbouring tokens.
+// A single renormalised slot (p = 1) gets exactly 0.
 template <lrmoe_dtype DT, bool SIGMOID, bool RENORM, int SUB>
 __global__ void __launch_bounds__(256) route_grad_sparse_kernel(const RouteGradParams p) {
   constexpr int kTokens = 32 / SUB;

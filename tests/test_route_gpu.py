@@ -304,3 +304,14 @@ def test_route_grad_takes_the_flat_dw_of_router_grad_and_torch_agrees():
     L.lrmoe_route_grad(z.detach().cuda(), torch.from_numpy(idx).cuda(), dw.cuda(), out)
     tol = (4 * spread(z.detach().numpy(), "softmax") + 150) * U * dw.abs().max().item()
     assert (out.cpu() - z.grad).abs().max().item() <= tol
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_route_grad_of_one_renormalised_slot_is_zero(kind, dt):
+    """Its weight is the constant scale, whatever the logits."""
+    z = logits(257, 60, dt, 9).cuda()
+    idx = torch.randint(0, 60, (257, 1), device="cuda", dtype=torch.int32)
+    dz = torch.full_like(z, float("nan"))
+    L.lrmoe_route_grad(z, idx, torch.randn(257, 1, device="cuda"), dz, score_fn=FN[kind], renormalise=True, scale=2.5)
+    assert (dz == 0).all()
