@@ -169,12 +169,20 @@ __device__ __forceinline__ void store_row32(const uint32_t (&r)[32], uint16_t* o
   }
 }
 
-// silu(g) * u.  The exponential and the reciprocal are good to a few ulp of fp32; the result is
-// rounded to bf16.
+// silu(g) * u = g r u for g >= 0 and (g h r) u h for g < 0, h = exp(-|g| / 2), r = 1 / (1 + h^2) in
+// [1/2, 1]: exp(-g) itself would overflow, and its reciprocal flush, from g = -87 on, where the product
+// with a large u is still a normal number.  |g| h stays below 3/4, so no factor overflows before the
+// result does.  h is the square of 2^(-|g| log2(e) / 4), which flushes only past |g| = 349 (the power of
+// -|g| / 2 itself would need its range extended there, three more instructions).  2^x and 1/x are good to 2
+// and 1 ulp of fp32 (2^-23) and x is off by 2^-23: 14 + |g| ulp in all, 1.1e-5 at |g| = 80; the result
+// is rounded to bf16.
 __device__ __forceinline__ float silu_times(float g, float u) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
-  return g * r * u;
+  float q, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(fabsf(g) * -0.36067376f));
+  const float h = q * q;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.0f)));
+  const float f = g >= 0.0f ? 1.0f : h;
+  return g * f * r * u * f;
 }
 
 // 32 values of columns [nb, nb + 32) added to r (columns >= N skipped; N % 8 == 0).  Plain
