@@ -204,6 +204,15 @@ constexpr int TY = BM / RI;   // thread rows
 constexpr int FT = 16 * TY;   // threads of a K group
 constexpr int LR = FT / 4;    // tile rows that the threads load in a pass
 
+// silu(g) * u = g / (1 + h^2) * u for g >= 0 and (g h / (1 + h^2)) u h for g < 0, h = exp(-|g| / 2): exp(-g)
+// overflows from g = -88.7 on, where the product with a large u is still a normal number.  |g| h stays
+// below 3/4, so no factor overflows before the result does.
+__device__ __forceinline__ float silu_times(float g, float u) {
+  const float h = expf(-0.5f * fabsf(g));
+  const float f = g >= 0.0f ? 1.0f : h;
+  return g * f / fmaf(h, h, 1.0f) * u * f;
+}
+
 // Ring of FS slices of K, copied asynchronously as they lie in memory; rows padded by four
 // floats keep the 16-byte reads of neighbouring columns in different banks.  KS groups of FT threads
 // take 16 of a slice's k each and add up at the end.
@@ -368,7 +377,7 @@ __global__ void __launch_bounds__(KS * FT) fprop_simt_kernel(const FpropF32 p) {
             g += p.bias[(size_t)e * 2 * N + n];
             u += p.bias[(size_t)e * 2 * N + N + n];
           }
-          const float a = g * sigmoidf_(g) * u;
+          const float a = silu_times(g, u);
           if (p.g) p.g[at + n] = g;
           if (p.u) p.u[at + n] = u;
           if (p.a) p.a[at + n] = a;

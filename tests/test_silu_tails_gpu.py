@@ -48,7 +48,7 @@ def run(gates, ups, dt, rows, gather, bias=False):
 
 # rows: a one-SM tile, and tiles on SM pairs
 @pytest.mark.parametrize("rows,gather,bias", [(1, False, False), (300, False, True), (1, True, True), (300, True, False)])
-@pytest.mark.parametrize("dt", ["bf16"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_activation_over_the_range_of_the_gate(dt, rows, gather, bias):
     pairs = [(s * g, u) for g in GATES for s in (1, -1) for u in UPS]
     pairs += [(1.0, 1.0)] * (-len(pairs) % 8)
@@ -67,7 +67,7 @@ def test_activation_over_the_range_of_the_gate(dt, rows, gather, bias):
         assert np.isinf(row[inf]).all() and (np.sign(row[inf]) == np.sign(ref[inf])).all()
 
 
-@pytest.mark.parametrize("dt", ["bf16"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_activation_of_infinities_and_nan(dt):
     """As the formula g / (1 + exp(-g)) * u gives them.  (g and u are formed in a product with zeros, in which
     an infinite weight alone would become NaN, so they come by the bias.)"""
