@@ -294,8 +294,8 @@ __device__ __forceinline__ bool topk_by_threshold(const uint32_t (&key)[VPL], in
     if (in && at < 32) box[at] = ((uint64_t)key[i] << 32) | (uint32_t)~(lane * VPL + i);
     count += __popc(who);
   }
+  __syncwarp();  // box is written, also for order_fp64 after a selection by rounds
   if (count > 32) return false;
-  __syncwarp();
   const uint64_t own = lane < count ? box[lane] : 0ull;
   if (lane >= count) box[lane] = 0ull;
   __syncwarp();
