@@ -643,6 +643,18 @@ int lrmoe_selftest_gemm_stall(const void* rows, int rows_cap, const void* W,
                               const int32_t* offsets, int E, int K, int N, void* out, int two_sm,
                               uint32_t limit_us, uint32_t* status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Diagnostic (no counterpart in the pages): lrmoe_grouped_bias_grad (bf16
+ * rows) launched so that every CTA withholds the first copy of its run of rows,
+ * with every device-side wait limited to limit_us microseconds (1 .. 1 000 000).
+ * The wait for that copy runs out, the kernel raises LRMOE_ST_TIMEOUT, lets the
+ * copies in flight land and returns without further waiting; db is then
+ * invalid, and the context stays usable.  status is required.
+ * ------------------------------------------------------------------------- */
+int lrmoe_selftest_bias_grad_stall(const void* grad_rows, int rows_cap, const int32_t* offsets,
+                                   int E, int N, float* db, uint32_t limit_us, uint32_t* status,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -722,6 +722,24 @@ int lrmoe_selftest_gemm_stall(const void* rows, int rows_cap, const void* W,
   return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_selftest_gemm_stall launch");
 }
 
+int lrmoe_selftest_bias_grad_stall(const void* grad_rows, int rows_cap, const int32_t* offsets,
+                                   int E, int N, float* db, uint32_t limit_us, uint32_t* status,
+                                   void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(status != nullptr && (reinterpret_cast<uintptr_t>(status) & 3u) == 0,
+          "status is null or misaligned");
+  REQUIRE(limit_us >= 1 && limit_us <= 1000000u, "limit_us=%u outside [1, 1000000]", limit_us);
+  REQUIRE(E > 0 && E <= kMaxGroupedExperts && rows_cap > 0, "E or rows_cap out of range");
+  if (int r = check_feature(N, LRMOE_BF16, "N")) return r;
+  REQUIRE_PTR(grad_rows);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(db);
+  const char* why = "lrmoe_selftest_bias_grad_stall launch";
+  cudaError_t e = launch_bias_grad(grad_rows, rows_cap, offsets, E, N, LRMOE_BF16, db, 0, status,
+                                   static_cast<cudaStream_t>(stream), &why, 1000ull * limit_us);
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, why);
+}
+
 int lrmoe_pruned_backward(const lrmoe_buffers* b, int T, int k, int E, int H, int I,
                           int rows_cap, lrmoe_dtype dt, void* stream) {
   g_last_error[0] = 0;

@@ -25,11 +25,12 @@ constexpr int kSlots = 6;
 constexpr int kBiasThreads = 256 + 32;  // 8 adding warps, one copying warp
 constexpr int kMaxSplits = 8;           // the portable cluster size
 
-template <lrmoe_dtype DT>
+// STALL: the diagnostic, in which every CTA withholds its first box and waits give up after stall_ns.
+template <lrmoe_dtype DT, bool STALL>
 __global__ void __launch_bounds__(kBiasThreads) bias_grad_kernel(
     const __grid_constant__ CUtensorMap tm /* rows as 16-bit columns, 64 x 64 boxes */,
     const int32_t* __restrict__ offsets, int N, float* __restrict__ db, int accumulate, int rows_cap,
-    int splits, uint32_t* __restrict__ status) {
+    int splits, uint64_t stall_ns, uint32_t* __restrict__ status) {
   constexpr int PER = DT == LRMOE_BF16 ? 8 : 4;  // values per 16-byte vector
   constexpr int COLS = 8 * PER;
   extern __shared__ uint8_t smem_raw[];
@@ -37,8 +38,9 @@ __global__ void __launch_bounds__(kBiasThreads) bias_grad_kernel(
                                              ~uintptr_t(1023));
   __shared__ uint64_t full[kSlots], empty[kSlots];
   __shared__ float total[COLS];
-  __shared__ int abort_word;
+  __shared__ int abort_word, stopped;  // stopped: boxes issued, if not all
   volatile int* abort_flag = &abort_word;
+  const uint64_t limit_ns = STALL ? stall_ns : kWaitLimitNs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
@@ -46,6 +48,7 @@ __global__ void __launch_bounds__(kBiasThreads) bias_grad_kernel(
       mbar_init(&empty[i], 8);
     }
     *abort_flag = 0;
+    stopped = 0x7fffffff;
     fence_barrier_init();
     tma_prefetch_desc(&tm);
   }
@@ -72,8 +75,11 @@ __global__ void __launch_bounds__(kBiasThreads) bias_grad_kernel(
       for (int b = 0; b < boxes; ++b) {
         const int slot = b % kSlots;
         if (b >= kSlots &&
-            !mbar_wait_bounded(&empty[slot], ((b / kSlots) & 1) ^ 1, abort_flag, status))
+            !mbar_wait_bounded(&empty[slot], ((b / kSlots) & 1) ^ 1, abort_flag, status, limit_ns)) {
+          stopped = b;
           break;
+        }
+        if (STALL && b == 0) continue;
         mbar_arrive_expect_tx(&full[slot], kBoxBytes);
         tma_load_2d(ring + slot * kBoxBytes, &tm, &full[slot], chunk * 64, r0 + lo + b * kBoxRows);
       }
@@ -97,7 +103,7 @@ __global__ void __launch_bounds__(kBiasThreads) bias_grad_kernel(
     int slot = 0;
     uint32_t phase = 0;
     for (int b = 0; b < boxes; ++b) {
-      if (!__all_sync(kFull, mbar_wait_bounded(&full[slot], phase, abort_flag, status))) break;
+      if (!__all_sync(kFull, mbar_wait_bounded(&full[slot], phase, abort_flag, status, limit_ns))) break;
       const uint4 v0 = *reinterpret_cast<const uint4*>(at + slot * kBoxBytes);
       const uint4 v1 = *reinterpret_cast<const uint4*>(at + slot * kBoxBytes + 32 * 128);
       __syncwarp();
@@ -114,8 +120,11 @@ __global__ void __launch_bounds__(kBiasThreads) bias_grad_kernel(
   __syncthreads();
   // a CTA whose wait ran out lets its copies land before it leaves its shared memory
   if (*abort_flag) {
-    if (threadIdx.x == 0)
-      for (int i = 0; i < kSlots; ++i) mbar_wait_drain(&full[i], 0), mbar_wait_drain(&full[i], 1);
+    if (threadIdx.x == 0) {  // of each slot the last box that was started
+      const int issued = min(boxes, stopped);
+      for (int b = max(issued - kSlots, STALL ? 1 : 0); b < issued; ++b)
+        mbar_wait_drain(&full[b % kSlots], (b / kSlots) & 1);
+    }
     __syncthreads();
   }
   __shared__ float part[8][COLS];
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(kBiasThreads) bias_grad_kernel(
 
 cudaError_t launch_bias_grad(const void* rows, int rows_cap, const int32_t* offsets, int E, int N,
                              lrmoe_dtype dt, float* db, int accumulate, uint32_t* status,
-                             cudaStream_t s, const char** why) {
+                             cudaStream_t s, const char** why, uint64_t stall_ns) {
   // the copies see 16-bit columns whatever the type
   const uint64_t cols = (uint64_t)N * (dt == LRMOE_BF16 ? 1 : 2);
   CUtensorMap tm;
@@ -172,7 +181,8 @@ cudaError_t launch_bias_grad(const void* rows, int rows_cap, const int32_t* offs
   while (splits < kMaxSplits && units * splits < 8ll * num_sms() &&
          (long long)rows_cap / ((long long)E * splits) >= 4 * kBoxRows)
     splits *= 2;
-  auto kern = dt == LRMOE_BF16 ? bias_grad_kernel<LRMOE_BF16> : bias_grad_kernel<LRMOE_F32>;
+  auto kern = dt == LRMOE_BF16 ? bias_grad_kernel<LRMOE_BF16, false> : bias_grad_kernel<LRMOE_F32, false>;
+  if (stall_ns) kern = bias_grad_kernel<LRMOE_BF16, true>;
   const int smem = kSlots * kBoxBytes + 1024;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
@@ -190,7 +200,8 @@ cudaError_t launch_bias_grad(const void* rows, int rows_cap, const int32_t* offs
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm, offsets, N, db, accumulate, rows_cap, splits, status);
+  return cudaLaunchKernelEx(&cfg, kern, tm, offsets, N, db, accumulate, rows_cap, splits, stall_ns,
+                            status);
 }
 
 }  // namespace lrmoe

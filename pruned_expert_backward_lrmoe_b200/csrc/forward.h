@@ -17,7 +17,7 @@ cudaError_t launch_combine(const void* y, const int32_t* idx, const float* w, in
                            cudaStream_t s);
 cudaError_t launch_bias_grad(const void* rows, int rows_cap, const int32_t* offsets, int E, int N,
                              lrmoe_dtype dt, float* db, int accumulate, uint32_t* status,
-                             cudaStream_t s, const char** why);
+                             cudaStream_t s, const char** why, uint64_t stall_ns = 0);
 cudaError_t launch_swiglu_simt(const void* x, int n_src, int src_div, const int32_t* perm,
                                const int32_t* offsets, int rows_cap, const void* W,
                                const void* bias, int E, int H, int I, void* Ap, void* g, void* u,

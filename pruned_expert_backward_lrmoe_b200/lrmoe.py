@@ -34,7 +34,8 @@ EXPORTS = ("lrmoe_version", "lrmoe_status_string", "lrmoe_last_error", "lrmoe_sc
            "lrmoe_grouped_dgrad_swiglu_gather", "lrmoe_grouped_wgrad_gather", "lrmoe_gather_rows",
            "lrmoe_group_received", "lrmoe_pack_wide", "lrmoe_split_wide",
            "lrmoe_selftest_gemm_stall", "lrmoe_route", "lrmoe_route_grad", "lrmoe_grouped_swiglu",
-           "lrmoe_grouped_linear", "lrmoe_grouped_bias_grad", "lrmoe_combine")
+           "lrmoe_grouped_linear", "lrmoe_grouped_bias_grad", "lrmoe_combine",
+           "lrmoe_selftest_bias_grad_stall")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -101,6 +102,7 @@ def load() -> ctypes.CDLL:
     lib.lrmoe_grouped_linear.argtypes = [P, I, P, P, P, I, I, I, I, P, P, I, P, P, P]
     lib.lrmoe_grouped_bias_grad.argtypes = [P, I, P, I, I, I, P, I, P, P]
     lib.lrmoe_combine.argtypes = [P, P, P, I, I, I, I, I, P, P, P, P]
+    lib.lrmoe_selftest_bias_grad_stall.argtypes = [P, I, P, I, I, P, U32, P, P]
     lib.lrmoe_pruned_backward.argtypes = [ctypes.POINTER(lrmoe_buffers), I, I, I, I, I, I, I, P]
     _lib = lib
     return lib
@@ -478,6 +480,17 @@ def lrmoe_selftest_gemm_stall(rows, W, offsets, out, two_sm: bool, limit_us: int
     _check(load().lrmoe_selftest_gemm_stall(_ptr(rows), rows.shape[0], _ptr(W), _ptr(offsets), E,
                                             K, N, _ptr(out), int(bool(two_sm)), int(limit_us),
                                             _ptr(status), _stream(stream)))
+
+
+def lrmoe_selftest_bias_grad_stall(grad_rows, offsets, db, limit_us: int, status, stream=None) -> None:
+    """Diagnostic: the bias gradient (bf16 rows) with the first copy of every run of rows withheld."""
+    E, N = db.shape
+    rows_cap, dev = grad_rows.shape[0], grad_rows.get_device()
+    r = _arg("grad_rows", grad_rows, torch.bfloat16, (rows_cap, N), dev)
+    off = _arg("offsets", offsets, torch.int32, (E + 1,), dev)
+    out = _arg("db", db, torch.float32, (E, N), dev)
+    _check(load().lrmoe_selftest_bias_grad_stall(r, rows_cap, off, E, N, out, int(limit_us),
+                                                 _status(status, dev), _launch(dev, stream)))
 
 
 def lrmoe_selftest_bounded_wait(limit_us: int, status, stream=None) -> None:
