@@ -26,7 +26,11 @@
  *     the grouped GEMMs use for dynamic tile scheduling (each launch takes the
  *     next pair and leaves it zeroed, so up to 64 grouped-GEMM launches may be
  *     in flight at once on one device), and the scratch array of
- *     lrmoe_select_quota_noalloc.  Calls are thread-safe on the host.
+ *     lrmoe_select_quota_noalloc.  A captured launch of those GEMMs (dgrad,
+ *     wgrad, their fused and gathering forms, lrmoe_pruned_backward) keeps the
+ *     pair it got at capture: a graph that holds them must not run at the same
+ *     time as another such graph or as other grouped-GEMM launches, since two
+ *     launches on one pair skip tiles.  Calls are thread-safe on the host.
  *   - Calls only enqueue work on `stream` and never synchronise the host.
  *     Counts and offsets stay on the device; later kernels read them there.
  *   - Errors a host can see (null pointer, size <= 0, feature size not a
@@ -469,8 +473,9 @@ int lrmoe_unpack(const void* dXp, int rows_cap, const int32_t* pos, int T, int k
  *   lrmoe_select_quota(score = topk_w) -> lrmoe_grouped_swiglu ->
  *   lrmoe_grouped_linear -> lrmoe_combine,
  * and leaves topk_idx, topk_w, g, u, a in the layouts of lrmoe_pruned_backward
- * and y in that of lrmoe_router_grad.  None of these calls keeps any state
- * between launches.
+ * and y in that of lrmoe_router_grad.  None of these calls, nor
+ * the gradients below, keeps any state between launches (but what the caller's
+ * workspace holds).
  *
  * lrmoe_route: experts and weights of every token from router logits
  * z [T][E] in dtype dt (rows contiguous; E need not be a multiple of 8).
