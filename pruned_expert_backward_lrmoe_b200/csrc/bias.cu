@@ -4,15 +4,18 @@
 // wgrad of the pruned backward.)
 //
 // HBM-bound: every row is read once.  A cluster of CTAs owns an (expert, 128-byte chunk of
-// columns); its CTAs take neighbouring runs of the expert's rows, since an expert with many rows
-// would otherwise be one CTA's long tail, and a single expert only a few CTAs.  A CTA's rows come
+// columns); its CTAs take neighbouring runs of the expert's rows.  Their number comes from the host,
+// which knows only the mean length of an expert: clusters serve few experts and columns, so that a
+// single expert is not a few CTAs' work.  With many of both there is one CTA to an (expert, chunk)
+// however long the expert is, and a long one is their tail.  A CTA's rows come
 // in through a ring of 6 TMA boxes of 64 rows x 128 bytes (48 KB on the way, four CTAs per SM):
 // most of a typical expert's run is requested at once, which plain loads into registers could not
 // hold.  Each of 256 threads adds two 16-byte vectors per box; a column's sums meet in the warp
 // (shuffles), then over the eight warps, then over the cluster's CTAs through distributed shared
-// memory, each in a fixed order.  No atomics, no workspace.  65536 rows of 1536 over 128 experts:
-// 38 us, 5.3 TB/s (plain 16-byte loads, eight in flight: 59 us); 16381 rows of 4096 of one expert:
-// 27 us, 4.9 TB/s.
+// memory, each in a fixed order: a sum of m rows in one CTA is m / 32 additions deep and 18 more.  No
+// atomics, no workspace.  65536 rows of 1536 over 128 experts: 38 us, 5.3 TB/s (plain 16-byte loads,
+// eight in flight: 59 us), half of them in one expert: 126 us; 16381 rows of 4096 of one expert: 27 us,
+// 4.9 TB/s.
 #include "forward.h"
 #include "gemm_common.cuh"
 
@@ -175,8 +178,8 @@ cudaError_t launch_bias_grad(const void* rows, int rows_cap, const int32_t* offs
     return cudaErrorInvalidValue;
   }
   const long long units = (long long)E * (long long)((cols + 63) / 64);
-  // Split an expert's rows over a cluster while there are fewer than eight CTAs per SM and a CTA
-  // would still have a few boxes of rows on average.
+  // Split the experts' rows over clusters while there are fewer than eight CTAs per SM and a CTA
+  // would still have a few boxes of rows on average (the lengths themselves stay on the device).
   int splits = 1;
   while (splits < kMaxSplits && units * splits < 8ll * num_sms() &&
          (long long)rows_cap / ((long long)E * splits) >= 4 * kBoxRows)
