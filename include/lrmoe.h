@@ -503,7 +503,9 @@ int lrmoe_unpack(const void* dXp, int rows_cap, const int32_t* pos, int T, int k
  * expert named twice counts twice).  With d_j = scale * dw_j, S = sum of the
  * slots' s:  renormalised d_j <- (d_j - sum_i d_i s_i / S) / S;  D_e = sum of d_j
  * over the slots of e;  softmax dz_e = s_e (D_e - sum_f D_f s_f), sigmoid
- * dz_e = D_e s_e (1 - s_e).  Sums in fp32, one rounding to dt.  Empty slots are
+ * dz_e = D_e s_e (1 - s_e).  Sums in fp32, one rounding to dt: an element is good
+ * to fp32 relative to scale * max |dw| of its token, not to itself where its
+ * terms cancel.  Empty slots are
  * skipped (dw not read); ids >= E likewise and set LRMOE_ST_BAD_EXPERT; a slot
  * whose logit is not finite is skipped, and experts with such logits get 0
  * (NaN and +Inf set LRMOE_ST_NONFINITE where they are read: every logit with

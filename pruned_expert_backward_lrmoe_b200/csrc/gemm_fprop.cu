@@ -26,25 +26,28 @@
 // (32 a K block and CTA: more than the block's products take).  So their PAIR tile is DOUBLE: 256
 // rows x 512 columns, both accumulators at once, half the gathers per product.  For packed rows
 // (and on one SM) the two accumulators alternate and a tile's epilogue runs under the next
-// tile's products.  Single against DOUBLE, I = 768, T = 8192, gathered: H = 256 164 and 147 us,
-// 1024 315 and 300, T = 16384 H = 4096 I = 1408 3.07 and 2.86 ms; packed 2.53 and 2.70 ms.
+// tile's products.  Single against DOUBLE, E = 128, top-8, under load: I = 768, T = 8192, gathered:
+// H = 256 150 and 143 us, 1024 344 and 308, 2048 609 and 525; T = 16384, H = 4096, I = 1408 3.76 and
+// 3.23 ms (3.14 and 2.70 in the first passes, before the power cap settles); packed 3.10 and 3.17 ms.
 //
 // Every tile has the same K depth, so tiles are dealt out in turn; there is no device-side
 // scheduling state that two launches or two captured graphs could share.
 //
-// Roles: producer warps (one for packed rows; to gather, four share the four-row
-// gathers: with one warp the T = 16384 layer below took 6.8 ms), one warp for tensor memory and MMA issue, eight epilogue warps.  Every wait is bounded
-// (LRMOE_ST_TIMEOUT, then a clean exit).  No TMA multicast.
+// Roles: producer warps (one for packed rows; to gather, four share the four-row gathers: with
+// one warp the T = 16384 layer below took 6.8 ms), one warp for tensor memory and MMA issue, eight
+// epilogue warps.  Every wait is bounded (LRMOE_ST_TIMEOUT, then a clean exit).  No TMA multicast.
 //
 // What bounds it, and what it measured (B200, under load until the power cap settles):
 //   SwiGLU, T = 16384, E = 128, top-8, H = 4096, I = 1408, gathered rows: 3.2-3.4 ms (900-950
-//     TFLOP/s at 1.4 GHz, 1000 W: power); packed rows 2.9-3.1 ms; the same flops as one dense product
+//     TFLOP/s at 1.4 GHz, 1000 W: power); packed rows 3.1 ms; the same flops as one dense product
 //     2.34 ms, cuBLAS 2.29.
 //   linear, T = 8111, E = 128, top-8, K = 768, N = 2048: 0.26 ms, of which 45 us are the one-SM
 //     launch reading half of the weights again; without any epilogue 0.23.  One dense 16384 x 1408 x
 //     4096 product: 161 us, cuBLAS 151, without epilogue 143.
-//   SwiGLU, T = 16 (a few rows per expert), H = 2048, I = 768: 80-85 us, the weights of the experts
-//     taken at 6.2-6.6 TB/s (HBM).
+//   SwiGLU, T = 16 (a few rows per expert), H = 2048, I = 768: 80-86 us, linear, K = 768, N = 2048: 40 us;
+//     the weights of the experts taken at 6.1-6.6 TB/s (HBM).
+//   One expert that every token takes, T = 4096: SwiGLU, H = 2048, I = 1408 67 us (705 TFLOP/s), linear,
+//     K = 1408, N = 2048, residual 32 us (731): two turns of tiles, the second one partly empty.
 #include "forward.h"
 #include "gemm_common.cuh"
 
@@ -145,8 +148,8 @@ __device__ __forceinline__ void tma_gather4_pair(void* dst, const void* tmap, ui
 }
 
 // bf16 row segment [nb, nb + 32) of `orow`, columns >= N skipped.  wide: rows and columns lie on
-// 32 bytes, so a thread writes whole sectors (linear, K = 768, N = 2048: 240 us against 295 with
-// 16-byte stores).
+// 32 bytes, so a thread writes whole sectors (linear, T = 8111, K = 768, N = 2048: 263 us against
+// 293 with 16-byte stores; 217 and 247 in the first passes, before the power cap settles).
 __device__ __forceinline__ void store_row32(const uint32_t (&r)[32], uint16_t* orow, int nb, int N,
                                             bool wide) {
   if (!wide) {

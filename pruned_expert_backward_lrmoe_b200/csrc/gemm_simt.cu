@@ -189,7 +189,7 @@ struct FpropF32 {
 
 // 128 CUDA-core multiply-adds a cycle and SM are the limit for large layers; the layers that fp32
 // is for are small, and there the latency of a tile is: T = 1021, K = 256, N = 512, one expert,
-// residual: 14 us.
+// residual: 14.6 us; SwiGLU of 2042 pairs over 8 experts, H = 256, I = 384: 39.6 us, 20 TFLOP/s.
 //
 // Two fp32 multiply-adds in one instruction, each rounded as fmaf.
 __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {

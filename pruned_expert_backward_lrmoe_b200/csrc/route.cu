@@ -11,17 +11,22 @@
 // the score rises with the logit, so the logits themselves are compared.  Keys with a bias and
 // group values are computed in fp32 with a bound on their error; where that leaves the order open
 // (about one token in a thousand), the warp computes the keys of that token again in fp64 and
-// selects by those.
+// selects by those.  With a bias and k = 32 the lanes hold 32 experts and none is left for the best one
+// behind them, so the order is never known to be sure and every token of 32 or more open experts takes
+// that way.
 //
 // One warp per token.  Expert e = lane * VPL + i lives in register i of a lane, so the lowest
 // lane that holds a maximum holds the lowest expert.
 //
 // Bound by the latency and the number of a token's dependent steps (67-70% of the issue slots; the
-// bytes would take 1-2 us): T = 16384, E = 128, top-8: 9 us (440 instructions a token), with a bias,
-// sigmoid: 13 us (670); T = 16383, E = 256 in 8 groups, bias, sigmoid: 23 us (1040).  A token that goes
-// to fp64 takes 0.6 us more for the order of its slots, 3 us for its groups, 6 for all keys.  One
-// token: a launch.  Gradient, T = 16384, E = 128, top-8, renormalised: 7.7 us, latency and the 8.4 MB of
-// the result; softmax of 160 experts, not renormalised, T = 8191: 10 us.
+// bytes would take 1-2 us).  Passes over several sets of inputs, T = 16384, bf16: E = 128, top-8: 9 us (440
+// instructions a token), with a bias, sigmoid: 14.5 us (670); E = 256 in 8 groups, bias, sigmoid: 23 us
+// (1040), softmax 27.6 (its kernels of up to 256 experts spill 52-92 bytes, the sigmoid ones do not).  A token
+// that goes to fp64 takes 0.6 us more for the order of its slots, 3 us for its groups, 6 for all keys:
+// E = 128 with a bias, sigmoid, k = 31: 54 us, k = 32: 111.  Where more than 32 keys pass the threshold
+// (topk_by_threshold): E = 130, k = 16: 41 us, E = 300: 65.  One token: a launch.
+// Gradient, device time: T = 16384, E = 128, top-8, renormalised: 5.3 us; softmax, not renormalised, the same 10.1,
+// T = 8191, E = 160, bf16, top-6 5.9 us; latency and the bytes of the result.  A call takes 7.5 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -260,8 +265,11 @@ __device__ __noinline__ int topk_fp64(double* key, int E, int k, int lane) {
 }
 
 // The k experts of the largest keys in slot order, by threshold: at least k + 1 of the warp's keys
-// reach the (k + 1)-th largest of the 32 lane maxima, and few more do (11 or so of 128 for
-// k = 8).  Those that do are brought to one per lane and ranked by counting (key, lower
+// reach the (k + 1)-th largest of the 32 lane maxima, and few more do while k is well below the number
+// of lanes that hold experts (random logits, in the mean: 10 of 128 for k = 8, 22 for k = 16).  Lanes hold a
+// power of two of experts, so E = 130 and 300 leave 17 and 19 lanes: for k = 16 more than 32 keys pass
+// for 94% and 66% of the tokens (E = 72: 50%, 160: 39%, 384: 13%, 128 and 256: 0.2%; k <= 10: none).  Those that
+// do are brought to one per lane and ranked by counting (key, lower
 // expert first).  Lane j gets the j-th largest (mine, mine_key), for all that reach the threshold;
 // whole: no expert is left behind them.
 // False (nothing set) where more than 32 do.
