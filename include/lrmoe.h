@@ -85,7 +85,7 @@ typedef enum { LRMOE_SCORE_SOFTMAX = 0, LRMOE_SCORE_SIGMOID = 1 } lrmoe_score_fn
 /* Device status word bits. */
 #define LRMOE_ST_BAD_EXPERT 1u /* some topk_idx >= E (that pair was skipped) */
 #define LRMOE_ST_BAD_QUOTA  2u /* some quota < 0 (treated as 0) */
-#define LRMOE_ST_NONFINITE  4u /* some score, router logit or router bias was +Inf or NaN */
+#define LRMOE_ST_NONFINITE  4u /* some score, router logit, router bias, gradient or norm was +Inf or NaN */
 #define LRMOE_ST_TIMEOUT    8u /* a bounded device-side wait gave up; outputs invalid */
 #define LRMOE_ST_BAD_INDEX 16u /* an index (perm/pos entry; checked build: any) was out of range; skipped */
 
@@ -576,6 +576,119 @@ int lrmoe_grouped_bias_grad(const void* grad_rows, int rows_cap, const int32_t* 
 int lrmoe_combine(const void* y, const int32_t* topk_idx, const float* topk_w, int T, int k, int E,
                   int H, lrmoe_dtype dt, const void* residual, void* Y, uint32_t* status,
                   void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The router's auxiliary losses (the pages' subject is the skew of the experts'
+ * load, RU-A and FR-A; they name no loss against it): counts per expert, the
+ * balance loss and the z-loss of router logits z [T][E] and the routing
+ * topk_idx [T*k] that lrmoe_route took from them.
+ *
+ * Sequence b is the tokens t of [seq_offsets[b], seq_offsets[b+1]) (seq_offsets
+ * [B+1] int32 on the device, rising, within 0 .. T; NULL: B = 1, all T tokens).  A
+ * token counts if a slot of it names an expert (0 <= topk_idx < E) and it lies in
+ * a sequence: padded tokens have empty slots.  With
+ *   p_te = softmax(z_t)_e, or sigmoid(z_te) / sum_f sigmoid(z_tf)
+ *   c_be = the pairs of expert e, m_b = sum_e c_be, n_b = the tokens that count,
+ *   P_be = sum_t p_te / n_b, f_be = E c_be / m_b, B' = the sequences with n_b > 0,
+ *   N = sum_b n_b
+ * lrmoe_balance writes
+ *   counts [B][E] int32     c_be
+ *   stats [B+1][2] int32    (n_b, m_b); in the last row (N, B')
+ *   mean_score [B][E] fp32  P_be (0 where n_b = 0)
+ *   loss [2] fp32           coef / B' sum_b sum_e f_be P_be   (1 coef when balanced)
+ *                           z_coef / N sum_t (log sum_e exp z_te)^2; 0 without tokens
+ * lrmoe_balance_grad writes dlogits [T][E] in dt, the gradient of dloss[0] loss[0] +
+ * dloss[1] loss[1] (dloss [2] fp32 on the device, NULL: 1, 1; the counts have no
+ * gradient), from the counts and stats of lrmoe_balance for the same inputs:
+ *   D_te = dloss[0] coef f_be / (n_b B');  softmax dz_te = p_te (D_te - sum_f D_tf p_tf),
+ *   sigmoid that times 1 - sigmoid(z_te);
+ *   dz_te += dloss[1] z_coef 2 lse_t / N softmax(z_t)_e
+ * plus add [T][E] in dt (NULL: nothing; it may be dlogits itself: the gradient of
+ * lrmoe_route_grad).  Every row is written: tokens that do not count get add, or 0.
+ * One rounding to dt; an element is good to fp32 relative to the largest terms of
+ * its token, not to itself where its terms cancel.
+ *
+ * fp32 sums in a fixed order: the same inputs give the same bits.  A logit of
+ * -Inf has score 0 and gradient 0; NaN and +Inf count as -Inf and set
+ * LRMOE_ST_NONFINITE; a token with no finite logit still counts, with scores and z-loss
+ * of 0.  ids >= E are skipped and set LRMOE_ST_BAD_EXPERT.  seq_offsets that fall
+ * or leave 0 .. T set LRMOE_ST_BAD_INDEX (in lrmoe_balance), the results are then
+ * invalid.  Limits: k <= 32, E <= 1024, coef and z_coef finite.  dlogits must not
+ * overlap an input but add.  workspace: lrmoe_balance_workspace_bytes(T, E, B) bytes,
+ * of one call at a time; nothing in it outlives the call.
+ * ------------------------------------------------------------------------- */
+size_t lrmoe_balance_workspace_bytes(int T, int E, int B);
+int lrmoe_balance(const void* logits, int T, int E, lrmoe_dtype dt, const int32_t* topk_idx, int k,
+                  lrmoe_score_fn score_fn, const int32_t* seq_offsets, int B, float coef,
+                  float z_coef, int32_t* counts, int32_t* stats, float* mean_score, float* loss,
+                  void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+int lrmoe_balance_grad(const void* logits, int T, int E, lrmoe_dtype dt, const int32_t* topk_idx,
+                       int k, lrmoe_score_fn score_fn, const int32_t* seq_offsets, int B, float coef,
+                       float z_coef, const int32_t* counts, const int32_t* stats,
+                       const float* dloss, const void* add, void* dlogits, uint32_t* status,
+                       void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The step that the weight gradients are for (the pages end at the gradients), over
+ * many tensors at once.  `tensors` is a host array, read during the call; the pointers in
+ * it are device pointers to n contiguous values each, in any shape (lrmoe_pruned_backward's
+ * dW_gu and dW_down with the layer's W_gu and W_down, lrmoe_grouped_bias_grad's db, ...).
+ * Tensors of no values are passed over.  No two of them may overlap.
+ *
+ * lrmoe_grad_norm: out[0] = the 2-norm over all tensors' gradients together, out[1] =
+ * min(1, max_norm / out[0]) (out fp32 [2]; max_norm > 0, +Inf: no clipping).  Of the
+ * tensors only grad and n are read.  Squares are summed in 64 bits over partial sums of 16
+ * values in 32 bits (in 64 where those would leave their range), in a fixed order.  A
+ * norm that is not finite sets LRMOE_ST_NONFINITE and out[1] = 0.
+ *
+ * lrmoe_adamw, element by element in fp32, with t = the number of this step (from 1):
+ *   g <- grad_scale g                      (grad_scale fp32 [1] on the device, NULL: 1)
+ *   m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
+ *   p <- p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * lr and t are read on the device where lr_dev (fp32 [1]) and step_dev (int32 [1]) are
+ * given, so that a captured step can be replayed with others (a t below 1 counts as 1).  A grad_scale of 0 (the norm was
+ * not finite) leaves everything as it was.  An element whose new v is not finite (its gradient is not, or
+ * its square overflows) is left as it was and sets LRMOE_ST_NONFINITE.
+ *   param [n] in param_dt; with bf16, master [n] fp32 may hold the weights: p is then
+ *     read from and written to master, and param gets it rounded to nearest.
+ *   state_bits 32: m, v [n] fp32.  state_bits 8: m and v [n] hold e4m3 codes of m and of
+ *     sqrt(v), m_scale and v_scale [ceil(n / 256)] fp32 one scale to 256 neighbouring
+ *     values (value = code scale; scale = the largest magnitude / 448, at least 2^-126, 0
+ *     for a block of zeros; all zeros is the state before the first step).  p takes m and
+ *     v as they are before they are rounded.
+ * What is kept in fewer bits than 32 without a copy (8-bit states, bf16 weights without
+ * master) is rounded at random to one of its two neighbours, so that it is right on average:
+ * to nearest, a value whose step is below half its spacing would never move, and sqrt(v) moves by
+ * less than (1 - beta2) / 2 of itself a step where v shrinks.  The upper neighbour in
+ * magnitude is taken with the chance of the value's place between the two, by
+ *   h(x): x ^= x >> 16; x *= 0x9E3779B1; x ^= x >> 15; x *= 0x6A09E667; x ^= x >> 16  (mod 2^32)
+ *   key = h(h(h(seed) + t) + i), w = h(key + (e mod 2^32) + (e / 2^32) 0x632BE5AB)
+ * for value e of tensor i: the low 16 bits of w for m, its high 16 bits for sqrt(v), the
+ * high 16 bits of w 0x9E3779B1 mod 2^32 for p.  A nonzero sqrt(v) is never held as 0 but at
+ * least as the smallest code 2^-9 (an m over a v of 0 would be a step of m / eps).
+ * 0 <= beta1, beta2 < 1, eps > 0, lr, weight_decay >= 0, all finite; step >= 1.
+ * grad may not be written by the call; it and the others may not overlap.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* param;         /* [n] in param_dt */
+  float* master;       /* [n] or NULL: the weights in 32 bits (bf16 param; all tensors or none) */
+  const void* grad;    /* [n] in grad_dt */
+  void* m;             /* [n] fp32, or e4m3 codes */
+  void* v;             /* [n] fp32, or e4m3 codes of sqrt(v) */
+  float* m_scale;      /* [ceil(n / 256)], 8-bit states only */
+  float* v_scale;
+  int64_t n;
+  float weight_decay;
+} lrmoe_tensor;
+
+size_t lrmoe_grad_norm_workspace_bytes(int count);
+int lrmoe_grad_norm(const lrmoe_tensor* tensors, int count, lrmoe_dtype grad_dt, float max_norm,
+                    float* out, void* workspace, size_t workspace_bytes, uint32_t* status,
+                    void* stream);
+int lrmoe_adamw(const lrmoe_tensor* tensors, int count, lrmoe_dtype param_dt, lrmoe_dtype grad_dt,
+                int state_bits, float lr, const float* lr_dev, double beta1, double beta2, float eps,
+                int step, const int32_t* step_dev, const float* grad_scale, uint32_t seed,
+                uint32_t* status, void* stream);
 
 /* ---------------------------------------------------------------------------
  * The whole path a1..a5 on one stream (RU-B bullets 3-5): score, selection,

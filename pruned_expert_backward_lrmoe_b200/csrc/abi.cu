@@ -10,6 +10,7 @@
 #include "../../include/lrmoe.h"
 #include "forward.h"
 #include "launch.h"
+#include "step.h"
 
 namespace lrmoe {
 
@@ -738,6 +739,141 @@ int lrmoe_selftest_bias_grad_stall(const void* grad_rows, int rows_cap, const in
   cudaError_t e = launch_bias_grad(grad_rows, rows_cap, offsets, E, N, LRMOE_BF16, db, 0, status,
                                    static_cast<cudaStream_t>(stream), &why, 1000ull * limit_us);
   return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, why);
+}
+
+size_t lrmoe_balance_workspace_bytes(int T, int E, int B) {
+  if (T <= 0 || E <= 0 || B <= 0 || E > kMaxGroupedExperts) return 0;
+  return balance_workspace(T, E, B);
+}
+
+static int check_balance(int T, int E, lrmoe_dtype dt, int k, lrmoe_score_fn score_fn,
+                         const int32_t* seq_offsets, int B, float coef, float z_coef) {
+  REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  REQUIRE(valid_score_fn(score_fn), "unknown score function %d", (int)score_fn);
+  if (int r = check_pairs(T, k, E)) return r;
+  if (E > kMaxGroupedExperts) return fail(LRMOE_ERR_UNSUPPORTED, "E=%d > %d", E, kMaxGroupedExperts);
+  REQUIRE(B > 0 && (seq_offsets != nullptr || B == 1),
+          "B=%d must be positive, and 1 without seq_offsets", B);
+  REQUIRE((long long)B * E < (1LL << 31) - 1, "B*E overflows int32");
+  REQUIRE(aligned16(seq_offsets), "seq_offsets is not 16-byte aligned");
+  REQUIRE(coef - coef == 0.0f && z_coef - z_coef == 0.0f, "coef and z_coef must be finite");
+  return LRMOE_OK;
+}
+
+int lrmoe_balance(const void* logits, int T, int E, lrmoe_dtype dt, const int32_t* topk_idx, int k,
+                  lrmoe_score_fn score_fn, const int32_t* seq_offsets, int B, float coef,
+                  float z_coef, int32_t* counts, int32_t* stats, float* mean_score, float* loss,
+                  void* workspace, size_t workspace_bytes, uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  if (int r = check_balance(T, E, dt, k, score_fn, seq_offsets, B, coef, z_coef)) return r;
+  REQUIRE_PTR(logits);
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(stats);
+  REQUIRE_PTR(mean_score);
+  REQUIRE_PTR(loss);
+  const size_t need = balance_workspace(T, E, B);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(LRMOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  REQUIRE(aligned16(workspace), "workspace is not 16-byte aligned");
+  cudaError_t e = launch_balance(logits, T, E, dt, topk_idx, k, score_fn, seq_offsets, B, coef, z_coef,
+                                 counts, stats, mean_score, loss, workspace, status,
+                                 static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_balance launch");
+}
+
+int lrmoe_balance_grad(const void* logits, int T, int E, lrmoe_dtype dt, const int32_t* topk_idx,
+                       int k, lrmoe_score_fn score_fn, const int32_t* seq_offsets, int B, float coef,
+                       float z_coef, const int32_t* counts, const int32_t* stats,
+                       const float* dloss, const void* add, void* dlogits, uint32_t* status,
+                       void* stream) {
+  g_last_error[0] = 0;
+  if (int r = check_balance(T, E, dt, k, score_fn, seq_offsets, B, coef, z_coef)) return r;
+  REQUIRE_PTR(logits);
+  REQUIRE_PTR(topk_idx);
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(stats);
+  REQUIRE((reinterpret_cast<uintptr_t>(dloss) & 3u) == 0, "dloss is not 4-byte aligned");
+  REQUIRE(aligned16(add), "add is not 16-byte aligned");
+  REQUIRE_PTR(dlogits);
+  REQUIRE(dlogits != logits, "dlogits must not be logits");
+  cudaError_t e = launch_balance_grad(logits, T, E, dt, topk_idx, k, score_fn, seq_offsets, B, coef,
+                                      z_coef, counts, stats, dloss, add, dlogits, status,
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_balance_grad launch");
+}
+
+static int check_tensor(const lrmoe_tensor& t, int i) {
+  REQUIRE(t.n >= 0 && t.n <= (1LL << 40), "tensor %d: n=%lld is negative or above 2^40", i,
+          (long long)t.n);
+  REQUIRE(t.n == 0 || (t.grad != nullptr && aligned16(t.grad)),
+          "tensor %d: grad is null or not 16-byte aligned", i);
+  return LRMOE_OK;
+}
+
+size_t lrmoe_grad_norm_workspace_bytes(int count) {
+  return count <= 0 ? 0 : grad_norm_workspace(count);
+}
+
+int lrmoe_grad_norm(const lrmoe_tensor* tensors, int count, lrmoe_dtype grad_dt, float max_norm,
+                    float* out, void* workspace, size_t workspace_bytes, uint32_t* status,
+                    void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(valid_dtype(grad_dt), "unknown dtype %d", (int)grad_dt);
+  REQUIRE(tensors != nullptr && count > 0, "tensors is null or count=%d is not positive", count);
+  REQUIRE(max_norm > 0.0f, "max_norm must be positive");
+  REQUIRE_PTR(out);
+  for (int i = 0; i < count; ++i)
+    if (int r = check_tensor(tensors[i], i)) return r;
+  const size_t need = grad_norm_workspace(count);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(LRMOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  REQUIRE(aligned16(workspace), "workspace is not 16-byte aligned");
+  cudaError_t e = launch_grad_norm(tensors, count, grad_dt, max_norm, out, workspace, status,
+                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_grad_norm launch");
+}
+
+int lrmoe_adamw(const lrmoe_tensor* tensors, int count, lrmoe_dtype param_dt, lrmoe_dtype grad_dt,
+                int state_bits, float lr, const float* lr_dev, double beta1, double beta2, float eps,
+                int step, const int32_t* step_dev, const float* grad_scale, uint32_t seed,
+                uint32_t* status, void* stream) {
+  g_last_error[0] = 0;
+  REQUIRE(valid_dtype(param_dt), "unknown dtype %d", (int)param_dt);
+  REQUIRE(valid_dtype(grad_dt), "unknown dtype %d", (int)grad_dt);
+  REQUIRE(state_bits == 32 || state_bits == 8, "state_bits=%d must be 32 or 8", state_bits);
+  REQUIRE(tensors != nullptr && count > 0, "tensors is null or count=%d is not positive", count);
+  REQUIRE(lr >= 0.0f && lr - lr == 0.0f, "lr must be finite and not negative");
+  REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0,
+          "beta1 and beta2 must be in [0, 1)");
+  REQUIRE(eps > 0.0f && eps - eps == 0.0f, "eps must be finite and positive");
+  REQUIRE(step_dev != nullptr || step >= 1, "step=%d must be positive", step);
+  REQUIRE(((reinterpret_cast<uintptr_t>(lr_dev) | reinterpret_cast<uintptr_t>(step_dev) |
+            reinterpret_cast<uintptr_t>(grad_scale)) & 3u) == 0,
+          "lr_dev, step_dev or grad_scale is not 4-byte aligned");
+  bool any_master = false, any_without = false;
+  for (int i = 0; i < count; ++i) {
+    const lrmoe_tensor& t = tensors[i];
+    if (int r = check_tensor(t, i)) return r;
+    REQUIRE(t.weight_decay >= 0.0f && t.weight_decay - t.weight_decay == 0.0f,
+            "tensor %d: weight_decay must be finite and not negative", i);
+    if (t.n == 0) continue;
+    REQUIRE(t.param != nullptr && aligned16(t.param), "tensor %d: param is null or not 16-byte aligned", i);
+    REQUIRE(t.m != nullptr && aligned16(t.m) && t.v != nullptr && aligned16(t.v),
+            "tensor %d: m or v is null or not 16-byte aligned", i);
+    REQUIRE(state_bits == 32 || (t.m_scale != nullptr && t.v_scale != nullptr &&
+                                 ((reinterpret_cast<uintptr_t>(t.m_scale) |
+                                   reinterpret_cast<uintptr_t>(t.v_scale)) & 3u) == 0),
+            "tensor %d: m_scale or v_scale is null or not 4-byte aligned", i);
+    REQUIRE(aligned16(t.master), "tensor %d: master is not 16-byte aligned", i);
+    (t.master != nullptr ? any_master : any_without) = true;
+  }
+  REQUIRE(!any_master || !any_without, "master is given for some tensors only");
+  REQUIRE(!any_master || param_dt == LRMOE_BF16, "master goes with bf16 parameters only");
+  AdamwArgs a{lr, beta1, beta2, eps, step, lr_dev, step_dev, grad_scale, seed, status};
+  cudaError_t e = launch_adamw(tensors, count, param_dt, grad_dt, state_bits, a,
+                               static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LRMOE_OK : cuda_fail(e, "lrmoe_adamw launch");
 }
 
 int lrmoe_pruned_backward(const lrmoe_buffers* b, int T, int k, int E, int H, int I,

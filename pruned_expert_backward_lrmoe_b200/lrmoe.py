@@ -35,7 +35,8 @@ EXPORTS = ("lrmoe_version", "lrmoe_status_string", "lrmoe_last_error", "lrmoe_sc
            "lrmoe_group_received", "lrmoe_pack_wide", "lrmoe_split_wide",
            "lrmoe_selftest_gemm_stall", "lrmoe_route", "lrmoe_route_grad", "lrmoe_grouped_swiglu",
            "lrmoe_grouped_linear", "lrmoe_grouped_bias_grad", "lrmoe_combine",
-           "lrmoe_selftest_bias_grad_stall")
+           "lrmoe_selftest_bias_grad_stall", "lrmoe_balance_workspace_bytes", "lrmoe_balance",
+           "lrmoe_balance_grad", "lrmoe_grad_norm_workspace_bytes", "lrmoe_grad_norm", "lrmoe_adamw")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -51,6 +52,12 @@ class lrmoe_buffers(ctypes.Structure):
         "score", "counts", "kept", "offsets", "perm", "pos",
         "Xp", "DYp", "Ap", "Gp", "Up", "dGUp", "dXp", "dW_gu", "dW_down", "dX",
         "workspace")] + [("workspace_bytes", ctypes.c_size_t), ("status", ctypes.c_void_p)]
+
+
+class lrmoe_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale",
+                                               "v_scale")] + [("n", ctypes.c_int64),
+                                                              ("weight_decay", ctypes.c_float)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -103,6 +110,15 @@ def load() -> ctypes.CDLL:
     lib.lrmoe_grouped_bias_grad.argtypes = [P, I, P, I, I, I, P, I, P, P]
     lib.lrmoe_combine.argtypes = [P, P, P, I, I, I, I, I, P, P, P, P]
     lib.lrmoe_selftest_bias_grad_stall.argtypes = [P, I, P, I, I, P, U32, P, P]
+    lib.lrmoe_balance_workspace_bytes.argtypes = [I, I, I]
+    lib.lrmoe_balance_workspace_bytes.restype = Z
+    lib.lrmoe_balance.argtypes = [P, I, I, I, P, I, I, P, I, F, F, P, P, P, P, P, Z, P, P]
+    lib.lrmoe_balance_grad.argtypes = [P, I, I, I, P, I, I, P, I, F, F, P, P, P, P, P, P, P]
+    lib.lrmoe_grad_norm_workspace_bytes.argtypes = [I]
+    lib.lrmoe_grad_norm_workspace_bytes.restype = Z
+    lib.lrmoe_grad_norm.argtypes = [P, I, I, F, P, P, Z, P, P]
+    D = ctypes.c_double
+    lib.lrmoe_adamw.argtypes = [P, I, I, I, I, F, P, D, D, F, I, P, P, U32, P, P]
     lib.lrmoe_pruned_backward.argtypes = [ctypes.POINTER(lrmoe_buffers), I, I, I, I, I, I, I, P]
     _lib = lib
     return lib
@@ -471,6 +487,171 @@ def lrmoe_combine(y, topk_idx, topk_w, E: int, Y, residual=None, status=None, st
     r = _arg("residual", residual, dt, (T, H), dev)
     _check(load().lrmoe_combine(yp, i, w, T, k, int(E), H, _dt(y), r, o, _status(status, dev),
                                 _launch(dev, stream)))
+
+
+def lrmoe_balance_workspace_bytes(T: int, E: int, B: int = 1) -> int:
+    return int(load().lrmoe_balance_workspace_bytes(T, E, B))
+
+
+def _sequences(seq_offsets, dev: int):
+    """Number of sequences and the address of their offsets (None: one sequence of all tokens)."""
+    if seq_offsets is None:
+        return 1, None
+    B = seq_offsets.numel() - 1
+    return B, _arg("seq_offsets", seq_offsets, torch.int32, (B + 1,), dev)
+
+
+def _workspace(t: torch.Tensor, dev: int):
+    return _arg("workspace", t, torch.uint8, (t.numel(),), dev), t.numel()
+
+
+def lrmoe_balance(logits, topk_idx, counts, stats, mean_score, loss, workspace, seq_offsets=None,
+                  score_fn: int = LRMOE_SCORE_SOFTMAX, coef: float = 1.0, z_coef: float = 0.0,
+                  status=None, stream=None) -> None:
+    """Pairs per expert counts [B][E], tokens and pairs per sequence stats [B+1][2], mean_score [B][E]
+    and loss [2] = (balance loss, z-loss) of router logits [T][E] and their routing [T][k], for the B
+    sequences that seq_offsets [B+1] bounds (None: one)."""
+    T, E = logits.shape
+    k = topk_idx.shape[-1]
+    dev = logits.get_device()
+    z = _arg("logits", logits, logits.dtype, (T, E), dev)
+    i = _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    B, off = _sequences(seq_offsets, dev)
+    c = _arg("counts", counts, torch.int32, (B, E), dev)
+    st = _arg("stats", stats, torch.int32, (B + 1, 2), dev)
+    ms = _arg("mean_score", mean_score, torch.float32, (B, E), dev)
+    lo = _arg("loss", loss, torch.float32, (2,), dev)
+    ws, n = _workspace(workspace, dev)
+    _check(load().lrmoe_balance(z, T, E, _dt(logits), i, k, int(score_fn), off, B, coef, z_coef, c,
+                                st, ms, lo, ws, n, _status(status, dev), _launch(dev, stream)))
+
+
+def lrmoe_balance_grad(logits, topk_idx, counts, stats, dlogits, seq_offsets=None,
+                       score_fn: int = LRMOE_SCORE_SOFTMAX, coef: float = 1.0, z_coef: float = 0.0,
+                       dloss=None, add=None, status=None, stream=None) -> None:
+    """dlogits [T][E] = the gradient of dloss [2] . loss, for lrmoe_balance's inputs, counts and stats,
+    plus add [T][E] (which may be dlogits itself)."""
+    T, E = logits.shape
+    k = topk_idx.shape[-1]
+    dev = logits.get_device()
+    z = _arg("logits", logits, logits.dtype, (T, E), dev)
+    i = _arg("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    B, off = _sequences(seq_offsets, dev)
+    c = _arg("counts", counts, torch.int32, (B, E), dev)
+    st = _arg("stats", stats, torch.int32, (B + 1, 2), dev)
+    dl = _arg("dloss", dloss, torch.float32, (2,), dev)
+    ad = _arg("add", add, logits.dtype, (T, E), dev)
+    dz = _arg("dlogits", dlogits, logits.dtype, (T, E), dev)
+    _check(load().lrmoe_balance_grad(z, T, E, _dt(logits), i, k, int(score_fn), off, B, coef, z_coef,
+                                     c, st, dl, ad, dz, _status(status, dev), _launch(dev, stream)))
+
+
+class TensorList:
+    """The tensors of lrmoe_grad_norm and lrmoe_adamw, checked once and kept: gradients and, for a
+    step, parameters, states m and v (lists of the same length; see alloc_adamw), their scales for
+    8-bit states, and 32-bit copies `master` of bf16 parameters.  Any shapes; weight_decay is one
+    number or one for each tensor.  The calls address the tensors' memory as it was when the list was
+    made."""
+
+    def __init__(self, grads, params=None, m=None, v=None, master=None, m_scale=None, v_scale=None,
+                 weight_decay=0.0):
+        self.count = len(grads)
+        if self.count == 0:
+            raise ValueError("no tensors")
+        if (params is None) != (m is None) or (params is None) != (v is None):
+            raise ValueError("params, m and v go together")
+        if params is None and not (master is None and m_scale is None and v_scale is None):
+            raise ValueError("master, m_scale and v_scale go with params, m and v")
+        given = dict(grad=grads, param=params, m=m, v=v, master=master, m_scale=m_scale, v_scale=v_scale)
+        for name, ts in given.items():
+            if ts is not None and len(ts) != self.count:
+                raise ValueError(f"{name}: {len(ts)} tensors, {self.count} gradients")
+        self.device = grads[0].get_device()
+        self.grad_dt = _dt(grads[0])
+        self.param_dt = self.state_bits = None
+        types = dict(grad=grads[0].dtype, master=torch.float32, m_scale=torch.float32,
+                     v_scale=torch.float32)
+        if params is not None:
+            self.param_dt = _dt(params[0])
+            if master is not None and self.param_dt != LRMOE_BF16:
+                raise ValueError("master goes with bf16 parameters only")
+            self.state_bits = 32 if m[0].dtype == torch.float32 else 8
+            if (self.state_bits == 8) != (m_scale is not None) or (m_scale is None) != (v_scale is None):
+                raise ValueError("m_scale and v_scale go with 8-bit (float8_e4m3fn) states")
+            types.update(param=params[0].dtype, m=m[0].dtype, v=m[0].dtype)
+            if types["m"] not in (torch.float32, torch.float8_e4m3fn):
+                raise ValueError(f"unsupported state dtype {types['m']}")
+        decay = [float(weight_decay)] * self.count if isinstance(weight_decay, (int, float)) \
+            else [float(w) for w in weight_decay]
+        if len(decay) != self.count:
+            raise ValueError(f"weight_decay: {len(decay)} values, {self.count} tensors")
+        self.tensors = (lrmoe_tensor * self.count)()
+        written = []  # (first, past the last address, name), of what a step writes and reads
+        for i, g in enumerate(grads):
+            t = self.tensors[i]
+            t.n, t.weight_decay = g.numel(), decay[i]
+            for name, ts in given.items():
+                if ts is None:
+                    continue
+                shape = (-(-t.n // 256),) if name.endswith("_scale") else g.shape
+                at = _arg(f"{name} {i}", ts[i], types[name], shape, self.device)
+                setattr(t, name, at)
+                if t.n and params is not None:
+                    written.append((at, at + ts[i].numel() * ts[i].element_size(), f"{name} {i}"))
+        written.sort()
+        for a, b in zip(written, written[1:]):
+            if b[0] < a[1]:
+                raise ValueError(f"{a[2]} and {b[2]} overlap")
+        self.kept = given  # the memory stays while the list does
+
+
+def alloc_adamw(params, state_bits: int = 32, master: bool = False) -> Dict[str, list]:
+    """States of lrmoe_adamw before the first step, as the arguments of TensorList: m and v (with
+    state_bits 8 also m_scale and v_scale), and with `master` 32-bit copies of the parameters."""
+    if state_bits not in (32, 8):
+        raise ValueError(f"state_bits must be 32 or 8, got {state_bits}")
+    kind = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+    zeros = lambda p: torch.zeros(p.shape, dtype=torch.uint8 if state_bits == 8 else kind,  # noqa: E731
+                                  device=p.device).view(kind)
+    out = {"m": [zeros(p) for p in params], "v": [zeros(p) for p in params]}
+    if state_bits == 8:
+        for name in ("m_scale", "v_scale"):
+            out[name] = [torch.zeros(-(-p.numel() // 256), dtype=torch.float32, device=p.device) for p in params]
+    if master:
+        out["master"] = [p.float() for p in params]
+    return out
+
+
+def lrmoe_grad_norm_workspace_bytes(count: int) -> int:
+    return int(load().lrmoe_grad_norm_workspace_bytes(count))
+
+
+def lrmoe_grad_norm(tensors: TensorList, out, workspace, max_norm: float = float("inf"), status=None,
+                    stream=None) -> None:
+    """out [2] = the 2-norm of all gradients together and min(1, max_norm / it)."""
+    dev = tensors.device
+    o = _arg("out", out, torch.float32, (2,), dev)
+    ws, n = _workspace(workspace, dev)
+    _check(load().lrmoe_grad_norm(tensors.tensors, tensors.count, tensors.grad_dt, max_norm, o, ws, n,
+                                  _status(status, dev), _launch(dev, stream)))
+
+
+def lrmoe_adamw(tensors: TensorList, lr, step, beta1: float = 0.9, beta2: float = 0.999,
+                eps: float = 1e-8, grad_scale=None, seed: int = 0, status=None, stream=None) -> None:
+    """One AdamW step over the list's tensors, in place.  lr and step (from 1) are numbers, or tensors
+    (fp32 [1], int32 [1]) that are read on the device; grad_scale (fp32 [1]) multiplies the gradients
+    (lrmoe_grad_norm's out[1:]); seed is for the random rounding of 8-bit states and of bf16
+    parameters without master."""
+    if tensors.param_dt is None:
+        raise ValueError("the list has gradients only")
+    dev = tensors.device
+    lr_dev = _arg("lr", lr, torch.float32, (1,), dev) if isinstance(lr, torch.Tensor) else None
+    step_dev = _arg("step", step, torch.int32, (1,), dev) if isinstance(step, torch.Tensor) else None
+    gs = _arg("grad_scale", grad_scale, torch.float32, (1,), dev)
+    _check(load().lrmoe_adamw(tensors.tensors, tensors.count, tensors.param_dt, tensors.grad_dt,
+                              tensors.state_bits, 0.0 if lr_dev else lr, lr_dev, beta1, beta2, eps,
+                              1 if step_dev else step, step_dev, gs, seed & 0xFFFFFFFF,
+                              _status(status, dev), _launch(dev, stream)))
 
 
 def lrmoe_selftest_gemm_stall(rows, W, offsets, out, two_sm: bool, limit_us: int, status,
