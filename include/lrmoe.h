@@ -637,7 +637,7 @@ int lrmoe_balance_grad(const void* logits, int T, int E, lrmoe_dtype dt, const i
  *
  * lrmoe_grad_norm: out[0] = the 2-norm over all tensors' gradients together, out[1] =
  * min(1, max_norm / out[0]) (out fp32 [2]; max_norm > 0, +Inf: no clipping).  Of the
- * tensors only grad and n are read.  Squares are summed in 64 bits over partial sums of 16
+ * tensors only grad and n are read.  Squares are summed in 64 bits over partial sums of 8
  * values in 32 bits (in 64 where those would leave their range), in a fixed order.  A
  * norm that is not finite sets LRMOE_ST_NONFINITE and out[1] = 0.
  *
@@ -666,7 +666,7 @@ int lrmoe_balance_grad(const void* logits, int T, int E, lrmoe_dtype dt, const i
  * for value e of tensor i: the low 16 bits of w for m, its high 16 bits for sqrt(v), the
  * high 16 bits of w 0x9E3779B1 mod 2^32 for p.  A nonzero sqrt(v) is never held as 0 but at
  * least as the smallest code 2^-9 (an m over a v of 0 would be a step of m / eps).
- * 0 <= beta1, beta2 < 1, eps > 0, lr, weight_decay >= 0, all finite; step >= 1.
+ * 0 <= beta1, beta2 < 1, eps >= 2^-126, lr, weight_decay >= 0, all finite; step >= 1.
  * grad may not be written by the call; it and the others may not overlap.
  * ------------------------------------------------------------------------- */
 typedef struct {

@@ -846,7 +846,7 @@ int lrmoe_adamw(const lrmoe_tensor* tensors, int count, lrmoe_dtype param_dt, lr
   REQUIRE(lr >= 0.0f && lr - lr == 0.0f, "lr must be finite and not negative");
   REQUIRE(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0,
           "beta1 and beta2 must be in [0, 1)");
-  REQUIRE(eps > 0.0f && eps - eps == 0.0f, "eps must be finite and positive");
+  REQUIRE(eps >= 1.17549435e-38f && eps - eps == 0.0f, "eps must be finite and at least 2^-126");
   REQUIRE(step_dev != nullptr || step >= 1, "step=%d must be positive", step);
   REQUIRE(((reinterpret_cast<uintptr_t>(lr_dev) | reinterpret_cast<uintptr_t>(step_dev) |
             reinterpret_cast<uintptr_t>(grad_scale)) & 3u) == 0,

@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlock = 256;          // values of a warp, and to a scale
-constexpr int kTile = 8 * kBlock;    // values of a block's turn
+constexpr int kRow = 8 * kBlock;     // values of the warps of a thread block, one block each
 constexpr int kNormBlocks = 148 * 8; // at most, of a launch
 
 constexpr int kFew = 24, kMany = 448;  // tensors of a launch: 1.8 KB or 32 KB of parameters
@@ -108,45 +108,6 @@ __device__ __forceinline__ void store4(void* at, long long i, int left, const fl
   }
 }
 
-// e4m3 codes
-__device__ __forceinline__ void load4_codes(const void* at, long long i, int left, float (&v)[4]) {
-  const uint8_t* a = static_cast<const uint8_t*>(at) + i;
-  uint32_t q = 0;
-  if (left >= 4) {
-    q = *reinterpret_cast<const uint32_t*>(a);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < left) q |= (uint32_t)a[j] << (8 * j);
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)(q >> (16 * j))));
-    float lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-    v[2 * j] = lo;
-    v[2 * j + 1] = hi;
-  }
-}
-
-__device__ __forceinline__ void store4_codes(void* at, long long i, int left, const float (&v)[4]) {
-  uint8_t* a = static_cast<uint8_t*>(at) + i;
-  unsigned short lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
-  const uint32_t q = lo | ((uint32_t)hi << 16);
-  if (left >= 4) {
-    *reinterpret_cast<uint32_t*>(a) = q;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < left) a[j] = (uint8_t)(q >> (8 * j));
-  }
-}
-
 // ---------------------------------------------------------------------------
 // norm
 // ---------------------------------------------------------------------------
@@ -174,7 +135,7 @@ __global__ void __launch_bounds__(kThreads)
   for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     at = find_item(list, count, at, tile);
     const Item& it = list.t[at];
-    const long long base = (long long)(tile - (at ? list.t[at - 1].end : 0u)) * kTile + warp * kBlock + lane * 4;
+    const long long base = (long long)(tile - (at ? list.t[at - 1].end : 0u)) * kRow + warp * kBlock + lane * 4;
     float g[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -220,19 +181,6 @@ __global__ void __launch_bounds__(1024) norm_finish_kernel(const double* __restr
 // ---------------------------------------------------------------------------
 // AdamW
 // ---------------------------------------------------------------------------
-struct Hyper {
-  float b1, a1, b2, a2;  // b and 1 - b
-  float eps;
-  float lr, rate, root;  // lr, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
-  double log_b1, log_b2;
-  const float* lr_dev;
-  const int32_t* step_dev;
-  const float* grad_scale;
-  uint32_t seed;
-  int step, first;  // `first`: number of the launch's first tensor
-  uint32_t* status;
-};
-
 __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   h ^= h >> 16;
   h *= 0x9E3779B1u;
@@ -241,17 +189,9 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   return h ^ (h >> 16);
 }
 
-// x in [0, 448] to one of its two e4m3 neighbours: 16 random bits are added to the 20 that are
-// dropped.  Below 2^-6 the values are 2^-9 apart, as they are from 2^-6 to 2^-5, where x is moved.
-__device__ __forceinline__ float round_code(float x, uint32_t bits16) {
-  const float low = x < 0.015625f ? 0.015625f : 0.0f;
-  const uint32_t b = __float_as_uint(x + low) + (bits16 << 4);
-  return __uint_as_float(b & 0xfff00000u) - low;
-}
-
 __device__ __forceinline__ float rcp_fast(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -265,11 +205,420 @@ __device__ __forceinline__ void scale_of(float top, float& scale, float& inv) {
   inv = top > 0.0f ? 1.0f / scale : 0.0f;
 }
 
+// Two values at a time.
+struct F2 {
+  uint64_t b;
+  F2() = default;
+  __device__ __forceinline__ F2(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(x), "f"(y)); }
+  __device__ __forceinline__ explicit F2(float x) : F2(x, x) {}
+  static F2 twice(float x) {
+    uint32_t u;
+    memcpy(&u, &x, 4);
+    F2 r;
+    r.b = u | ((uint64_t)u << 32);
+    return r;
+  }
+  __device__ __forceinline__ float x() const { return __uint_as_float((uint32_t)b); }
+  __device__ __forceinline__ float y() const { return __uint_as_float((uint32_t)(b >> 32)); }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 c) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(c.b));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 c) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(c.b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 c, F2 d) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(c.b), "l"(d.b));
+  return r;
+}
+
+struct Hyper {
+  F2 b1, a1, b2, a2;  // b and 1 - b, each twice
+  F2 eps;
+  float lr, rate, root;  // lr, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  double log_b1, log_b2;
+  const float* lr_dev;
+  const int32_t* step_dev;
+  const float* grad_scale;
+  uint32_t seed;
+  int step, first;  // `first`: number of the launch's first tensor
+  uint32_t* status;
+};
+
+// four e4m3 codes
+__device__ __forceinline__ void codes4(uint32_t q, F2& a, F2& b) {
+  float f[4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)(q >> (16 * j))));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(f[2 * j]), "=f"(f[2 * j + 1])
+        : "r"(h));
+  }
+  a = F2(f[0], f[1]);
+  b = F2(f[2], f[3]);
+}
+
+__device__ __forceinline__ void load4_codes(const void* at, long long i, int left, float (&v)[4]) {
+  const uint8_t* a = static_cast<const uint8_t*>(at) + i;
+  uint32_t q = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < left) q |= (uint32_t)a[j] << (8 * j);
+  F2 lo, hi;
+  codes4(q, lo, hi);
+  v[0] = lo.x(), v[1] = lo.y(), v[2] = hi.x(), v[3] = hi.y();
+}
+
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// What a step computes of two values.  Each product and sum of m and v is rounded by itself: what is kept
+// in 8 bits depends on their last bits.
+struct Step {
+  F2 gs, root, rate, decay;  // rate and decay negative
+  const Hyper& hy;
+  template <int BITS>
+  __device__ __forceinline__ void moments(F2 g, F2 m, F2 v, F2 ms, F2 vs, F2& m1, F2& v1) const {
+    g = g * gs;
+    if constexpr (BITS == 8) {
+      m = m * ms;
+      v = v * vs;
+      v = v * v;
+    }
+    m1 = hy.b1 * m + hy.a1 * g;
+    v1 = hy.b2 * v + hy.a2 * g * g;
+  }
+  // the weights after the step, with r1 the root of v1
+  __device__ __forceinline__ F2 weights(F2 p, F2 m1, F2 r1) const {
+    const F2 den = fma2(r1, root, hy.eps);
+    return fma2(rate * m1, F2(rcp_fast(den.x()), rcp_fast(den.y())), fma2(decay, p, p));
+  }
+};
+
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// sqrt(v): y is 1/sqrt(s) to 22 bits or so, g = s y the root of s to as many, and g + (s - g^2) y / 2 that
+// root to the last bit but for one value in a million (the final correction of Markstein's square root, IBM
+// J. Res. Dev. 34, 1990).  s = 2^40 v is a normal number or 0, for which y takes 2^-126; it overflows from
+// v = 2^88 on.  g and the root are carried with a minus sign.
+__device__ __forceinline__ F2 root_of(F2 v, F2& s) {
+  s = fma2(v, F2(1099511627776.0f), F2(1.17549435e-38f));
+  const F2 t = v * F2(-1099511627776.0f);
+  const F2 y(rsqrt_fast(s.x()), rsqrt_fast(s.y()));
+  const F2 g = t * y;
+  return fma2(fma2(g, g, t), y * F2(0.5f), g) * F2(-9.5367431640625e-7f);
+}
+
+// |x| <= 448 to one of its two e4m3 neighbours: 16 random bits are added to the 20 of its magnitude that are
+// dropped.  Times 2^-120 the smallest normal code is the smallest normal number, so that the codes below it,
+// which are evenly spaced, come out of the same addition.
+__device__ __forceinline__ uint32_t round_bits(float x, uint32_t bits16) {
+  return (__float_as_uint(x) + (bits16 << 4)) & 0xfff00000u;
+}
+
+__device__ __forceinline__ unsigned short codes_of(F2 v) {
+  unsigned short q;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(v.y()), "f"(v.x()));
+  return q;
+}
+
+constexpr float kDown = 7.52316385e-37f, kUp = 1.32922800e+36f;  // 2^-120, 2^120
+
+// Codes of m and r >= 0 by random words; im, iv: the inverse scales times 2^-120.
+__device__ __forceinline__ unsigned short m_codes(F2 m, F2 im, uint32_t w0, uint32_t w1) {
+  const F2 y = m * im;
+  return codes_of(F2(__uint_as_float(round_bits(y.x(), w0 & 0xffffu)),
+                     __uint_as_float(round_bits(y.y(), w1 & 0xffffu))) * F2(kUp));
+}
+
+// SMALL: there may be roots below the smallest code: those become it, but for 0.
+template <bool SMALL>
+__device__ __forceinline__ unsigned short r_codes(F2 r, F2 iv, uint32_t w0, uint32_t w1) {
+  const F2 y = r * iv;
+  float a = y.x(), c = y.y();
+  if (SMALL) {
+    a = r.x() > 0.0f ? fmaxf(a, kDown * 0.001953125f) : 0.0f;
+    c = r.y() > 0.0f ? fmaxf(c, kDown * 0.001953125f) : 0.0f;
+  }
+  return codes_of(F2(__uint_as_float(round_bits(a, w0 >> 16)), __uint_as_float(round_bits(c, w1 >> 16))) * F2(kUp));
+}
+
+// bf16 bits of p in the high half, by the random bits of w
+__device__ __forceinline__ uint32_t random_bf16(float p, uint32_t w) {
+  return __float_as_uint(p) + ((w * 0x9E3779B1u) >> 16);
+}
+
+// Where a lane's values of a block lie.
+struct Place {
+  const char* g;
+  char *p, *master, *m, *v;
+  float *m_scale, *v_scale;
+};
+
+template <lrmoe_dtype PDT, bool MASTER, lrmoe_dtype GDT, int BITS>
+struct Block {
+  static constexpr bool kRandomParam = PDT == LRMOE_BF16 && !MASTER;
+  static constexpr bool kRandom = BITS == 8 || kRandomParam;
+  static constexpr lrmoe_dtype KDT = MASTER ? LRMOE_F32 : PDT;  // of the kept weights
+  // A lane's eight values: side by side with 8-bit states, whose vectors are then 8 bytes; else four of each
+  // half of the block, so that a warp's 16-byte vectors lie side by side.
+  static constexpr int kLane = BITS == 8 ? 8 : 4;   // values from one lane's to the next one's
+  static constexpr int kHalf = BITS == 8 ? 4 : 128; // from a lane's first four to its others
+
+  // eight values of a type as they lie in memory
+  template <lrmoe_dtype DT>
+  struct Raw {
+    static constexpr int kSize = DT == LRMOE_BF16 ? 2 : 4;
+    uint32_t u[2 * kSize];
+    __device__ __forceinline__ void load(const char* at) {
+      if constexpr (DT == LRMOE_F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 q = *reinterpret_cast<const uint4*>(at + h * kHalf * 4);
+          u[4 * h] = q.x, u[4 * h + 1] = q.y, u[4 * h + 2] = q.z, u[4 * h + 3] = q.w;
+        }
+      } else if constexpr (kHalf == 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(at);
+        u[0] = q.x, u[1] = q.y, u[2] = q.z, u[3] = q.w;
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint2 q = *reinterpret_cast<const uint2*>(at + h * kHalf * 2);
+          u[2 * h] = q.x, u[2 * h + 1] = q.y;
+        }
+      }
+    }
+    __device__ __forceinline__ F2 pair(int i) const {
+      if constexpr (DT == LRMOE_F32) return F2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+      return F2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    }
+  };
+  template <lrmoe_dtype DT>
+  static __device__ __forceinline__ void store(char* at, const F2 (&v)[4]) {
+    if constexpr (DT == LRMOE_F32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float4*>(at + h * kHalf * 4) =
+            make_float4(v[2 * h].x(), v[2 * h].y(), v[2 * h + 1].x(), v[2 * h + 1].y());
+    } else {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = pack_bf16x2(v[i].x(), v[i].y());
+      store_halves(at, b);
+    }
+  }
+  static __device__ __forceinline__ void store_halves(char* at, const uint32_t (&b)[4]) {
+    if constexpr (kHalf == 4) {
+      *reinterpret_cast<uint4*>(at) = make_uint4(b[0], b[1], b[2], b[3]);
+    } else {
+      *reinterpret_cast<uint2*>(at) = make_uint2(b[0], b[1]);
+      *reinterpret_cast<uint2*>(at + kHalf * 2) = make_uint2(b[2], b[3]);
+    }
+  }
+
+  struct Loaded {
+    Raw<GDT> g;
+    Raw<KDT> p;
+    Raw<BITS == 8 ? LRMOE_BF16 : LRMOE_F32> m, v;  // codes: u[0] and u[1]
+    float ms, vs;
+    __device__ __forceinline__ void load(const Place& at) {
+      g.load(at.g);
+      p.load(MASTER ? at.master : at.p);
+      if constexpr (BITS == 8) {
+        const uint2 a = *reinterpret_cast<const uint2*>(at.m), b = *reinterpret_cast<const uint2*>(at.v);
+        m.u[0] = a.x, m.u[1] = a.y;
+        v.u[0] = b.x, v.u[1] = b.y;
+        ms = *at.m_scale;
+        vs = *at.v_scale;
+      } else {
+        m.load(at.m);
+        v.load(at.v);
+      }
+    }
+  };
+
+  // A whole block.  False, and nothing written, if one of its values is to be left as it was or is out of the
+  // range that the short forms below are for.
+  static __device__ __forceinline__ bool whole(const Place& at, int lane, const Step& st, uint32_t key) {
+    Loaded in;
+    in.load(at);
+    F2 p1[4], m1[4], v1[4], r1[4], sum(0.0f);
+    float least = INFINITY;
+    if constexpr (BITS == 8) {
+      codes4(in.m.u[0], m1[0], m1[1]);
+      codes4(in.m.u[1], m1[2], m1[3]);
+      codes4(in.v.u[0], v1[0], v1[1]);
+      codes4(in.v.u[1], v1[2], v1[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BITS == 32) {
+        m1[i] = in.m.pair(i);
+        v1[i] = in.v.pair(i);
+      }
+      st.moments<BITS>(in.g.pair(i), m1[i], v1[i], F2(in.ms), F2(in.vs), m1[i], v1[i]);
+      F2 s;
+      r1[i] = root_of(v1[i], s);
+      sum = sum + s;
+      p1[i] = st.weights(in.p.pair(i), m1[i], r1[i]);
+      if constexpr (BITS == 8) least = min3(least, r1[i].x(), r1[i].y());
+    }
+    if (__any_sync(kFull, !(sum.x() + sum.y() < INFINITY))) return false;
+    float sm, sv, im, iv;
+    if constexpr (BITS == 8) {
+      float top_m = 0.0f, top_r = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        top_m = max3_abs(top_m, m1[i].x(), m1[i].y());
+        top_r = max3_abs(top_r, r1[i].x(), r1[i].y());
+      }
+      top_m = warp_max_abs(top_m);
+      top_r = warp_max_abs(top_r);
+      // the inverse scales times 2^-120 have to be normal numbers
+      if (fmaxf(top_m, top_r) > 16384.0f) return false;
+      scale_of(top_m, sm, im);
+      scale_of(top_r, sv, iv);
+    }
+    uint32_t w[8];
+    if constexpr (kRandom) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = mix(key + (uint32_t)(i / 4 * kHalf + i % 4));
+    }
+    if constexpr (MASTER) store<LRMOE_F32>(at.master, p1);
+    if constexpr (kRandomParam) {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[i] = __byte_perm(random_bf16(p1[i].x(), w[2 * i]), random_bf16(p1[i].y(), w[2 * i + 1]), 0x7632);
+      store_halves(at.p, b);
+    } else {
+      store<PDT>(at.p, p1);
+    }
+    if constexpr (BITS == 32) {
+      store<LRMOE_F32>(at.m, m1);
+      store<LRMOE_F32>(at.v, v1);
+    } else {
+      if (lane == 0) {
+        *at.m_scale = sm;
+        *at.v_scale = sv;
+      }
+      const F2 fm(im * kDown), fv(iv * kDown);
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = m_codes(m1[i], fm, w[2 * i], w[2 * i + 1]);
+      *reinterpret_cast<uint2*>(at.m) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+      if (__all_sync(kFull, least * iv >= 0.001953125f)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = r_codes<false>(r1[i], fv, w[2 * i], w[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = r_codes<true>(r1[i], fv, w[2 * i], w[2 * i + 1]);
+      }
+      *reinterpret_cast<uint2*>(at.v) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    }
+    return true;
+  }
+
+  // The same where values are missing or to be left as they were.  True if any is.
+  static __device__ __forceinline__ bool part(const Item& it, long long first, int lane, const Step& st,
+                                           uint32_t key /* of the block's first value */) {
+    const long long base = first + lane * 4;
+    bool bad = false;
+    float ms = 1.0f, vs = 1.0f;
+    if constexpr (BITS == 8) {
+      ms = it.m_scale[first / kBlock];
+      vs = it.v_scale[first / kBlock];
+    }
+    float p[2][4], m[2][4], v[2][4];
+    float top_m = 0.0f, top_r = 0.0f;
+    for (int h = 0; h < 2; ++h) {
+      const long long i = base + 128 * h;
+      const int left = (int)min(max(it.n - i, 0ll), 4ll);
+      float g[4];
+      load4<GDT>(it.g, i, left, g);
+      load4<KDT>(MASTER ? static_cast<const void*>(it.master) : it.p, i, left, p[h]);
+      if constexpr (BITS == 32) {
+        load4<LRMOE_F32>(it.m, i, left, m[h]);
+        load4<LRMOE_F32>(it.v, i, left, v[h]);
+      } else {
+        load4_codes(it.m, i, left, m[h]);
+        load4_codes(it.v, i, left, v[h]);
+      }
+      for (int j = 0; j < 4; ++j) {
+        F2 m1, v1;
+        st.moments<BITS>(F2(g[j]), F2(m[h][j]), F2(v[h][j]), F2(ms), F2(vs), m1, v1);
+        const float r1 = __fsqrt_rn(v1.x());
+        const bool ok = v1.x() < INFINITY;
+        bad |= !ok;
+        if (ok) p[h][j] = st.weights(F2(p[h][j]), m1, F2(r1)).x();
+        m[h][j] = ok ? m1.x() : m[h][j] * ms;
+        v[h][j] = !ok ? v[h][j] * vs : BITS == 8 ? r1 : v1.x();
+        top_m = fmaxf(top_m, fabsf(m[h][j]));
+        top_r = fmaxf(top_r, v[h][j]);
+      }
+    }
+    float im = 0.0f, iv = 0.0f;
+    if constexpr (BITS == 8) {
+      scale_of(warp_max_abs(top_m), ms, im);
+      scale_of(warp_max_abs(top_r), vs, iv);
+      if (lane == 0) {
+        it.m_scale[first / kBlock] = ms;
+        it.v_scale[first / kBlock] = vs;
+      }
+    }
+    for (int h = 0; h < 2; ++h) {
+      const long long i = base + 128 * h;
+      const int left = (int)min(max(it.n - i, 0ll), 4ll);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = kRandom ? mix(key + (uint32_t)(4 * lane + 128 * h + j)) : 0u;
+        if constexpr (BITS == 8) {
+          // in two steps: the inverse scale times 2^-120 may be no normal number
+          const unsigned short mq = m_codes(F2(m[h][j]) * F2(im), F2(kDown), w, w);
+          const float x = v[h][j] * iv;
+          const unsigned short vq = r_codes<true>(F2(v[h][j] > 0.0f ? fmaxf(x, 0.001953125f) : 0.0f), F2(kDown), w, w);
+          if (j < left) {
+            static_cast<uint8_t*>(it.m)[i + j] = (uint8_t)mq;
+            static_cast<uint8_t*>(it.v)[i + j] = (uint8_t)vq;
+          }
+        }
+        if constexpr (kRandomParam)
+          if (j < left) static_cast<unsigned short*>(it.p)[i + j] = (unsigned short)(random_bf16(p[h][j], w) >> 16);
+      }
+      if constexpr (MASTER) store4<LRMOE_F32>(it.master, i, left, p[h]);
+      if constexpr (!kRandomParam) store4<PDT>(it.p, i, left, p[h]);
+      if constexpr (BITS == 32) {
+        store4<LRMOE_F32>(it.m, i, left, m[h]);
+        store4<LRMOE_F32>(it.v, i, left, v[h]);
+      }
+    }
+    return bad;
+  }
+};
+
 template <lrmoe_dtype PDT, bool MASTER, lrmoe_dtype GDT, int BITS, int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 4 : 3)
     adamw_kernel(const __grid_constant__ Items<CAP> list, int count, const __grid_constant__ Hyper hy) {
-  constexpr bool kRandomParam = PDT == LRMOE_BF16 && !MASTER;
-  constexpr lrmoe_dtype KDT = MASTER ? LRMOE_F32 : PDT;  // of the kept weights
+  using B = Block<PDT, MASTER, GDT, BITS>;
   const unsigned tiles = list.t[count - 1].end;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ float shared_hyper[3];
@@ -292,105 +641,37 @@ __global__ void __launch_bounds__(kThreads)
     rate = shared_hyper[1];
     root = shared_hyper[2];
   }
+  Step st{F2(gs), F2(root), F2(-rate), F2(0.0f), hy};
   const uint32_t step_key = mix(mix(hy.seed) + (uint32_t)step);
   bool bad = false;
-  int at = 0;
+  int at = 0, known = -1;
+  uint32_t item_key = 0;
   for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     at = find_item(list, count, at, tile);
     const Item& it = list.t[at];
-    const long long first = (long long)(tile - (at ? list.t[at - 1].end : 0u)) * kTile + warp * kBlock;
+    if (at != known) {
+      known = at;
+      st.decay = F2(-(lr * it.decay));
+      if constexpr (B::kRandom) item_key = mix(step_key + (uint32_t)(hy.first + at));
+    }
+    const long long first = (long long)(tile - (at ? list.t[at - 1].end : 0u)) * kRow + warp * kBlock;
     if (first >= it.n) continue;
-    const long long base = first + lane * 4;
-    const float decay = lr * it.decay;
-    void* kept = MASTER ? static_cast<void*>(it.master) : it.p;
-    int left[2];
-    float g[2][4], p[2][4], m[2][4], v[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      left[h] = (int)min(max(it.n - base - 128 * h, 0ll), 4ll);
-      const long long i = base + 128 * h;
-      load4<GDT>(it.g, i, left[h], g[h]);
-      load4<KDT>(kept, i, left[h], p[h]);
-      if constexpr (BITS == 32) {
-        load4<LRMOE_F32>(it.m, i, left[h], m[h]);
-        load4<LRMOE_F32>(it.v, i, left[h], v[h]);
-      } else {
-        load4_codes(it.m, i, left[h], m[h]);
-        load4_codes(it.v, i, left[h], v[h]);
-      }
+    const uint32_t key = B::kRandom ? item_key + (uint32_t)first + (uint32_t)(first >> 32) * 0x632BE5ABu : 0u;
+    bool done = false;
+    if (it.n - first >= kBlock) {
+      constexpr int GS = GDT == LRMOE_BF16 ? 2 : 4, PS = PDT == LRMOE_BF16 ? 2 : 4, SS = BITS / 8;
+      const long long mine = first + B::kLane * lane;
+      Place to;
+      to.g = static_cast<const char*>(it.g) + mine * GS;
+      to.p = static_cast<char*>(it.p) + mine * PS;
+      to.master = MASTER ? reinterpret_cast<char*>(it.master + mine) : nullptr;
+      to.m = static_cast<char*>(it.m) + mine * SS;
+      to.v = static_cast<char*>(it.v) + mine * SS;
+      to.m_scale = BITS == 8 ? it.m_scale + first / kBlock : nullptr;
+      to.v_scale = BITS == 8 ? it.v_scale + first / kBlock : nullptr;
+      done = B::whole(to, lane, st, key + (uint32_t)(B::kLane * lane));
     }
-    float ms = 1.0f, vs = 1.0f;
-    if constexpr (BITS == 8) {
-      ms = it.m_scale[first / kBlock];
-      vs = it.v_scale[first / kBlock];
-    }
-    uint32_t key = 0;
-    if constexpr (BITS == 8 || kRandomParam) {
-      key = mix(step_key + (uint32_t)(hy.first + at));
-      key += (uint32_t)base + (uint32_t)(base >> 32) * 0x632BE5ABu;
-    }
-    float top_m = 0.0f, top_v = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float gg = g[h][j] * gs;
-        const float m0 = BITS == 8 ? __fmul_rn(m[h][j], ms) : m[h][j];
-        const float r0 = BITS == 8 ? v[h][j] * vs : 0.0f;
-        const float v0 = BITS == 8 ? __fmul_rn(r0, r0) : v[h][j];
-        // each product and sum rounded by itself, and an exact root: the codes depend on their last bits
-        const float m1 = __fadd_rn(__fmul_rn(hy.b1, m0), __fmul_rn(hy.a1, gg));
-        const float v1 = __fadd_rn(__fmul_rn(hy.b2, v0), __fmul_rn(__fmul_rn(hy.a2, gg), gg));
-        const bool ok = v1 < INFINITY;
-        bad |= !ok;
-        const float r1 = __fsqrt_rn(v1);
-        const float p0 = p[h][j];
-        const float p1 = fmaf(-rate * m1, rcp_fast(fmaf(r1, root, hy.eps)), fmaf(-decay, p0, p0));
-        m[h][j] = ok ? m1 : m0;
-        v[h][j] = BITS == 8 ? (ok ? r1 : r0) : (ok ? v1 : v0);
-        p[h][j] = ok ? p1 : p0;
-        if constexpr (BITS == 8) {
-          top_m = fmaxf(top_m, fabsf(m[h][j]));
-          top_v = fmaxf(top_v, fabsf(v[h][j]));
-        }
-      }
-    }
-    float im = 0.0f, iv = 0.0f;
-    if constexpr (BITS == 8) {
-      scale_of(warp_max_abs(top_m), ms, im);
-      scale_of(warp_max_abs(top_v), vs, iv);
-      if (lane == 0) {
-        it.m_scale[first / kBlock] = ms;
-        it.v_scale[first / kBlock] = vs;
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const long long i = base + 128 * h;
-      if constexpr (BITS == 8 || kRandomParam) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w = mix(key + 128 * h + j);
-          if constexpr (BITS == 8) {
-            m[h][j] = copysignf(round_code(fabsf(m[h][j]) * im, w & 0xffffu), m[h][j]);
-            const float x = v[h][j] * iv;
-            const float y = round_code(x, w >> 16);
-            v[h][j] = x > 0.0f ? fmaxf(y, 0.001953125f) : y;
-          }
-          if constexpr (kRandomParam)
-            p[h][j] = __uint_as_float((__float_as_uint(p[h][j]) + ((w * 0x9E3779B1u) >> 16)) & 0xffff0000u);
-        }
-      }
-      if constexpr (MASTER) store4<LRMOE_F32>(it.master, i, left[h], p[h]);
-      store4<PDT>(it.p, i, left[h], p[h]);
-      if constexpr (BITS == 32) {
-        store4<LRMOE_F32>(it.m, i, left[h], m[h]);
-        store4<LRMOE_F32>(it.v, i, left[h], v[h]);
-      } else {
-        store4_codes(it.m, i, left[h], m[h]);
-        store4_codes(it.v, i, left[h], v[h]);
-      }
-    }
+    if (!done) bad |= B::part(it, first, lane, st, key);
   }
   if (bad) raise_status(hy.status, LRMOE_ST_NONFINITE);
 }
@@ -406,7 +687,7 @@ int fill(Items<CAP>& list, const lrmoe_tensor* t, int count, int& next, int& fir
   first = next;
   for (; next < count && n < CAP; ++next) {
     const lrmoe_tensor& s = t[next];
-    const unsigned long long more = ((unsigned long long)s.n + kTile - 1) / kTile;
+    const unsigned long long more = ((unsigned long long)s.n + kRow - 1) / kRow;
     if (n > 0 && tiles + more > 0x7fffffffull) break;
     tiles += more;
     list.t[n++] = Item{s.param, s.master, s.grad, s.m, s.v, s.m_scale, s.v_scale, (long long)s.n,
@@ -477,11 +758,11 @@ auto pick(lrmoe_dtype gdt, int bits) {
 cudaError_t launch_adamw(const lrmoe_tensor* t, int count, lrmoe_dtype pdt, lrmoe_dtype gdt,
                          int bits, const AdamwArgs& a, cudaStream_t s) {
   Hyper h{};
-  h.b1 = (float)a.beta1;
-  h.a1 = (float)(1.0 - a.beta1);
-  h.b2 = (float)a.beta2;
-  h.a2 = (float)(1.0 - a.beta2);
-  h.eps = a.eps;
+  h.b1 = F2::twice((float)a.beta1);
+  h.a1 = F2::twice((float)(1.0 - a.beta1));
+  h.b2 = F2::twice((float)a.beta2);
+  h.a2 = F2::twice((float)(1.0 - a.beta2));
+  h.eps = F2::twice(a.eps);
   h.log_b1 = log(a.beta1);
   h.log_b2 = log(a.beta2);
   h.step = a.step < 1 ? 1 : a.step;
@@ -501,7 +782,7 @@ cudaError_t launch_adamw(const lrmoe_tensor* t, int count, lrmoe_dtype pdt, lrmo
     auto kern = pdt == LRMOE_F32 ? pick<LRMOE_F32, false, CAP>(gdt, bits)
                 : master         ? pick<LRMOE_BF16, true, CAP>(gdt, bits)
                                  : pick<LRMOE_BF16, false, CAP>(gdt, bits);
-    return launch_pdl(kern, dim3(grid_of(list, items, 8)), dim3(kThreads), 0, s, list, items, h);
+    return launch_pdl(kern, dim3(grid_of(list, items, 32)), dim3(kThreads), 0, s, list, items, h);
   });
 }
 

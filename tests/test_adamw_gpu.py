@@ -247,6 +247,24 @@ def test_random_rounding_is_right_on_average():
     assert abs(x.mean().item() - (1 - 7e-4)) < 5 * 0.5 * 2.0 ** -8 / math.sqrt(n) + 1e-6
 
 
+def test_root_is_that_of_cuda():
+    """The root behind the 8-bit states against torch's square root: a block of one value shows it as its scale.  It
+    is right to the last bit but where the root lies next to the middle of two numbers: less than one in 10^5."""
+    n = 1 << 18
+    g = torch.zeros(n, 256, device="cuda")
+    e = torch.empty(n, device="cuda").uniform_(-55, 40, generator=torch.Generator(device="cuda").manual_seed(2))
+    g[:, 5] = torch.exp2(e)
+    p = torch.zeros_like(g)
+    st = L.alloc_adamw([p], 8)
+    L.lrmoe_adamw(L.TensorList([g], [p], **st), lr=1e-3, step=1, beta1=0.9, beta2=0.9)
+    a2 = torch.tensor(1 - 0.9, device="cuda")
+    want = torch.sqrt(a2 * g[:, 5] * g[:, 5]) * (1 / torch.tensor(448.0))
+    got = st["v_scale"][0]
+    off = got != want
+    assert off.sum().item() <= n * 1e-5
+    assert ((got - want).abs() <= 2 * U * want).all()
+
+
 def test_rounding_depends_on_seed_and_step_alone():
     def after(seed, step, seed_of_data=0):
         t = Tensors([(5000,)], "bf16", bits=8, seed=seed_of_data)
