@@ -13,10 +13,17 @@
 // lie side by side.  A second kernel adds each sequence's rows in order (no atomics on floats: the
 // same inputs give the same bits) and its last block adds the losses up.
 //
-// A group of SUB lanes takes a token, VPL values to a lane; groups of a warp take neighbouring tokens.
+// A group of SUB lanes takes a token, VPL values to a lane; groups of a warp take neighbouring tokens.  Rows are
+// fetched an iteration ahead.  What bounds it: two special-function instructions to a sigmoid and one to an
+// exponential (16 a cycle and SM) and about 12 others to a value; with few tokens the chain of two launches.
+// Measured: 16384 x 128
+// fp32 softmax losses 9.4 us, gradient with a sum 5.4 us (25 MB: 4.7 TB/s); 65521 x 256 bf16 sigmoid losses of 29
+// sequences 23.8 us; gradient of 32749 x 250 bf16 sigmoid, 17 sequences, 13.6 us.
+#include <limits.h>
 #include <math.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "step.h"
 
 namespace lrmoe {
@@ -24,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxRuns = 592;  // runs of tokens: four blocks to an SM
+constexpr int kMaxRuns = 296;  // two blocks to an SM
 
 struct RowSums {  // of one piece of a run
   int tokens, pairs;
@@ -52,7 +59,7 @@ struct BalanceGradParams {
   const void* logits;
   const int32_t* idx;
   const int32_t* off;
-  int T, E, k, B;
+  int T, E, k, B, each;  // each: tokens of a warp
   float coef, z_coef;
   const int32_t *counts, *stats;
   const float* dloss;
@@ -61,79 +68,96 @@ struct BalanceGradParams {
   uint32_t* status;
 };
 
-// Values that a lane holds of a row: in vectors of 16 bytes, neighbouring lanes side by side, where rows
-// are whole vectors (the tensor starts on 16 bytes), else one by one.
-template <lrmoe_dtype DT, int VPL, int SUB, bool VEC>
+// Loads and stores under a condition, without a branch.
+template <int BYTES>
+__device__ __forceinline__ void load_if(bool on, const char* from, uint32_t* u) {
+  if constexpr (BYTES == 16)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t@p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3])
+        : "l"(from), "r"((int)on));
+  else if constexpr (BYTES == 4)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p ld.global.u32 %0, [%1];\n\t}"
+                 : "+r"(u[0])
+                 : "l"(from), "r"((int)on));
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p ld.global.u16 %0, [%1];\n\t}"
+                 : "+r"(u[0])
+                 : "l"(from), "r"((int)on));
+}
+
+template <int BYTES>
+__device__ __forceinline__ void store_if(bool on, char* to, const uint32_t* u) {
+  if constexpr (BYTES == 16)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t@p st.global.v4.u32 [%4], {%0, %1, %2, %3};\n\t}" ::"r"(u[0]),
+        "r"(u[1]), "r"(u[2]), "r"(u[3]), "l"(to), "r"((int)on)
+        : "memory");
+  else if constexpr (BYTES == 4)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p st.global.u32 [%1], %0;\n\t}" ::"r"(u[0]), "l"(to),
+                 "r"((int)on)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\t@p st.global.u16 [%1], %0;\n\t}" ::"r"(u[0]), "l"(to),
+                 "r"((int)on)
+                 : "memory");
+}
+
+// Values that a lane holds of a row: in vectors of G values, neighbouring lanes' side by side, where a row is
+// whole vectors (the tensor starts on 16 bytes).
+template <lrmoe_dtype DT, int VPL, int SUB, int G>
 struct Row {
-  static constexpr int G = DT == LRMOE_BF16 ? 8 : 4;  // values of a vector
-  static __device__ __forceinline__ int at(int i, int j) {
-    return VEC ? ((i / G) * SUB + j) * G + i % G : i * SUB + j;
+  static constexpr bool kPairs = DT == LRMOE_BF16 && G > 1;  // two values to a register
+  static constexpr int kSize = DT == LRMOE_BF16 ? 2 : 4, kBytes = G * kSize;
+  static constexpr int kOf = kPairs ? G / 2 : G;  // registers of a vector
+  struct Raw {
+    uint32_t u[kPairs ? VPL / 2 : VPL];
+  };
+  static __device__ __forceinline__ int at(int i, int j) { return ((i / G) * SUB + j) * G + i % G; }
+  static __device__ __forceinline__ uint32_t masked() {  // -inf
+    return DT == LRMOE_F32 ? 0xff800000u : 0xff80ff80u;
   }
-  // Values past the row's end, and all of them without `live`, are `none`.
-  static __device__ __forceinline__ void load(const void* z, size_t row, int E, int j, bool live,
-                                              float none, float (&v)[VPL]) {
-    if constexpr (VEC) {
+  // where lane j's first value of row t lies
+  static __device__ __forceinline__ size_t place(long long t, int E, int j) {
+    return ((size_t)t * E + (size_t)j * G) * kSize;
+  }
+  // The row as it lies in memory; values past its end, and all of them without `live`, are `none`.
+  static __device__ __forceinline__ void fetch(const char* from, int E, int j, bool live, uint32_t none, Raw& r) {
 #pragma unroll
-      for (int q = 0; q < VPL / G; ++q) {
-        const int e = (q * SUB + j) * G;
-        const bool ok = live && e < E;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (ok)
-          w = *reinterpret_cast<const uint4*>(static_cast<const char*>(z) + (row + e) * (16 / G));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    for (int q = 0; q < VPL / G; ++q) {
+      uint32_t* u = r.u + q * kOf;
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          float f;
-          if constexpr (DT == LRMOE_BF16)
-            f = (i & 1) ? __uint_as_float(u[i / 2] & 0xffff0000u) : bf16_bits_to_f32(u[i / 2] & 0xffffu);
-          else
-            f = __uint_as_float(u[i]);
-          v[q * G + i] = ok ? f : none;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = at(i, j);
-        float f = none;
-        if (live && e < E) {
-          if constexpr (DT == LRMOE_BF16)
-            f = bf16_bits_to_f32(static_cast<const unsigned short*>(z)[row + e]);
-          else
-            f = static_cast<const float*>(z)[row + e];
-        }
-        v[i] = f;
-      }
+      for (int i = 0; i < kOf; ++i) u[i] = none;
+      load_if<kBytes>(live && (q * SUB + j) * G < E, from + q * SUB * kBytes, u);
     }
   }
-  static __device__ __forceinline__ void store(void* z, size_t row, int E, int j, const float (&v)[VPL]) {
-    if constexpr (VEC) {
+  static __device__ __forceinline__ void unpack(const Raw& r, F2 (&v)[VPL / 2]) {
 #pragma unroll
-      for (int q = 0; q < VPL / G; ++q) {
-        const int e = (q * SUB + j) * G;
-        if (e >= E) continue;
-        uint4 w;
-        if constexpr (DT == LRMOE_BF16) {
-          const float* f = v + q * G;
-          w = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                         pack_bf16x2(f[6], f[7]));
+    for (int i = 0; i < VPL / 2; ++i) {
+      if constexpr (kPairs)
+        v[i] = F2(__uint_as_float(r.u[i] << 16), __uint_as_float(r.u[i] & 0xffff0000u));
+      else if constexpr (DT == LRMOE_BF16)
+        v[i] = F2(__uint_as_float(r.u[2 * i] << 16), __uint_as_float(r.u[2 * i + 1] << 16));
+      else
+        v[i] = F2(__uint_as_float(r.u[2 * i]), __uint_as_float(r.u[2 * i + 1]));
+    }
+  }
+  static __device__ __forceinline__ void store(char* to, int E, int j, bool live, const F2 (&v)[VPL / 2]) {
+#pragma unroll
+    for (int q = 0; q < VPL / G; ++q) {
+      uint32_t u[kOf];
+#pragma unroll
+      for (int i = 0; i < kOf; ++i) {
+        if constexpr (kPairs) {
+          const F2 f = v[(q * G) / 2 + i];
+          u[i] = pack_bf16x2(f.x(), f.y());
         } else {
-          const float* f = v + q * G;
-          w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                         __float_as_uint(f[3]));
+          const F2 f = v[(q * G + i) / 2];
+          const float x = (q * G + i) & 1 ? f.y() : f.x();
+          u[i] = DT == LRMOE_BF16 ? f32_to_bf16_bits_rne(x) : __float_as_uint(x);
         }
-        *reinterpret_cast<uint4*>(static_cast<char*>(z) + (row + e) * (16 / G)) = w;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = at(i, j);
-        if (e >= E) continue;
-        if constexpr (DT == LRMOE_BF16)
-          static_cast<unsigned short*>(z)[row + e] = (unsigned short)f32_to_bf16_bits_rne(v[i]);
-        else
-          static_cast<float*>(z)[row + e] = v[i];
-      }
+      store_if<kBytes>(live && (q * SUB + j) * G < E, to + q * SUB * kBytes, u);
     }
   }
 };
@@ -154,13 +178,15 @@ __device__ __forceinline__ float group_max(float v) {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// exp(x) for x <= 0 to 2^-21 or so of itself: x is a difference, so that its product's rounding is
-// small beside it
-__device__ __forceinline__ float exp_neg(float x) {
+__device__ __forceinline__ float ex2(float x) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * kLog2e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// exp(x) to 2^-21 or so of itself for x near 0; x = z - zmax is a difference, and sigmoids of |z| > 70 are done
+// in another way, so that the rounding of x log2 e stays small beside it
+__device__ __forceinline__ float exp_fast(float x) { return ex2(x * kLog2e); }
 
 __device__ __forceinline__ float rcp(float x) {
   float r;
@@ -168,77 +194,157 @@ __device__ __forceinline__ float rcp(float x) {
   return r;
 }
 
-// exp(z - zmax) of the group's row into u; its sum and zmax come back (0 and 0 for a row without a
+__device__ __forceinline__ float log_fast(float x) {  // x >= 1 here
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r * 0.693147180559945309f;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ float lane_max(const F2 (&v)[N]) {
+  float m = fmaxf(v[0].x(), v[0].y());
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = max3(m, v[i].x(), v[i].y());
+  return m;
+}
+
+template <int N>
+__device__ __forceinline__ float lane_sum(const F2 (&v)[N]) {
+  F2 s = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) s = s + v[i];
+  return s.x() + s.y();
+}
+
+template <int N>
+__device__ __forceinline__ float lane_dot(const F2 (&v)[N], const F2 (&w)[N]) {
+  F2 s = v[0] * w[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) s = fma2(v[i], w[i], s);
+  return s.x() + s.y();
+}
+
+// NaN and +inf count as -inf.
+template <int N>
+__device__ __forceinline__ void shut(F2 (&v)[N], uint32_t* status) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool x = v[i].x() < INFINITY, y = v[i].y() < INFINITY;
+    if (!x || !y) raise_status(status, LRMOE_ST_NONFINITE);
+    v[i] = F2(x ? v[i].x() : -INFINITY, y ? v[i].y() : -INFINITY);
+  }
+}
+
+// The group's sum of v, and of v D for the gradient, in one go.
+template <int SUB, int N>
+__device__ __forceinline__ float sum_and_dot(const F2 (&v)[N], const F2 (*D)[N], float* dot) {
+  if (D == nullptr) return group_sum<SUB>(lane_sum(v));
+  float s = lane_sum(v), d = lane_dot(v, *D);
+#pragma unroll
+  for (int o = SUB / 2; o >= 1; o >>= 1) {
+    s += __shfl_xor_sync(kFull, s, o);
+    d += __shfl_xor_sync(kFull, d, o);
+  }
+  *dot = d;
+  return s;
+}
+
+// exp(z - zmax) of U rows of the group in place; their sums and zmax come back (0 and 0 for a row without a
 // finite logit).  NaN and +inf are found by their sum, which is then no number: such rows, and those
-// without a finite logit, are done again with -inf in their place.
-template <int VPL, int SUB>
-__device__ __forceinline__ void softmax_terms(float (&v)[VPL], float (&u)[VPL], float& sum, float& zmax,
-                                              uint32_t* status) {
-  auto pass = [&]() {
-    float m = v[0];
+// without a finite logit, are read again with -inf in their place.  `again` reads row q.
+template <int N, int SUB, int U, typename Again>
+__device__ __forceinline__ void softmax_terms(F2 (&v)[U][N], float (&sum)[U], float (&zmax)[U],
+                                              uint32_t* status, Again&& again, const F2 (*D)[N] = nullptr,
+                                              float* dot = nullptr) {
+  auto pass = [&](int q) {
 #pragma unroll
-    for (int i = 1; i < VPL; ++i) m = fmaxf(m, v[i]);
-    zmax = group_max<SUB>(m);
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      u[i] = exp_neg(v[i] - zmax);
-      sum += u[i];
+    for (int i = 0; i < N; ++i) {
+      const F2 x = (v[q][i] + F2(-zmax[q])) * F2(kLog2e);
+      v[q][i] = F2(ex2(x.x()), ex2(x.y()));
     }
-    sum = group_sum<SUB>(sum);
   };
-  pass();
-  if (__any_sync(kFull, !(sum > 0.0f && sum < INFINITY))) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (!(v[i] < INFINITY)) {
-        raise_status(status, LRMOE_ST_NONFINITE);
-        v[i] = -INFINITY;
+  for (int q = 0; q < U; ++q) zmax[q] = group_max<SUB>(lane_max(v[q]));
+#pragma unroll
+  for (int q = 0; q < U; ++q) pass(q);
+  bool fine = true;
+#pragma unroll
+  for (int q = 0; q < U; ++q) {
+    sum[q] = sum_and_dot<SUB>(v[q], D, dot);
+    fine &= sum[q] > 0.0f && sum[q] < INFINITY;
+  }
+  if (__any_sync(kFull, !fine)) {
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      again(q);
+      shut(v[q], status);
+      zmax[q] = group_max<SUB>(lane_max(v[q]));
+      pass(q);
+      sum[q] = sum_and_dot<SUB>(v[q], D, dot);
+      if (!(zmax[q] > -INFINITY)) {
+        sum[q] = zmax[q] = 0.0f;
+        if (D != nullptr) *dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[q][i] = F2(0.0f);
       }
-    pass();
-    if (!(zmax > -INFINITY)) {
-      sum = zmax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) u[i] = 0.0f;
     }
   }
 }
 
-// sigmoid(z) of the group's row into u, all times one factor where their sum would be next to nothing;
-// their sum comes back (0 for a row without a finite logit).
-template <int VPL, int SUB>
-__device__ __forceinline__ void sigmoid_terms(float (&v)[VPL], float (&u)[VPL], float& sum,
-                                              uint32_t* status) {
-  bool bad = false;
-  float s = 0.0f;
+// s = sigmoid(z) of U rows of the group in place, a row all times one factor where its sum would be next to
+// nothing; their sums come back (0 for a row without a finite logit).  REST: 1 - s into `rest`, as exp(-z) s so
+// that it is as good near s = 1; where exp(-z) is infinite and s is 0 the minimum takes 1 and not their NaN.
+template <bool REST, int N, int SUB, int U, typename Again>
+__device__ __forceinline__ void sigmoid_terms(F2 (&v)[U][N], F2 (&rest)[REST ? U : 1][N], float (&sum)[U],
+                                              uint32_t* status, Again&& again, const F2 (*D)[N] = nullptr,
+                                              float* dot = nullptr) {
+  bool fine = true;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    bad |= !(v[i] < INFINITY);
-    const float t = exp_neg(-fabsf(v[i]));
-    const float r = rcp(1.0f + t);
-    u[i] = v[i] >= 0.0f ? r : t * r;
-    s += u[i];
-  }
-  sum = group_sum<SUB>(s);
-  if (__any_sync(kFull, bad || !(sum > 1e-30f))) {
-    float m = -INFINITY;
+  for (int q = 0; q < U; ++q) {
+    fine &= lane_max(v[q]) < INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (!(v[i] < INFINITY)) {
-        raise_status(status, LRMOE_ST_NONFINITE);
-        v[i] = -INFINITY;
+    for (int i = 0; i < N; ++i) {
+      const F2 x = v[q][i] * F2(-kLog2e);
+      const F2 t(ex2(x.x()), ex2(x.y()));
+      const F2 d = t + F2(1.0f);
+      v[q][i] = F2(rcp(d.x()), rcp(d.y()));
+      if constexpr (REST) {
+        const F2 w = t * v[q][i];
+        rest[q][i] = F2(fminf(w.x(), 1.0f), fminf(w.y(), 1.0f));
       }
-      m = fmaxf(m, v[i]);
     }
-    const float base = fminf(group_max<SUB>(m), 0.0f);  // the factor is exp(-base)
-    s = 0.0f;
+  }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const float t = exp_neg(-fabsf(v[i]));
-      u[i] = v[i] > -INFINITY ? exp_neg(fminf(v[i], 0.0f) - base) * rcp(1.0f + t) : 0.0f;
-      s += u[i];
+  for (int q = 0; q < U; ++q) {
+    sum[q] = sum_and_dot<SUB>(v[q], D, dot);
+    fine &= sum[q] > 1e-30f;
+  }
+  if (__any_sync(kFull, !fine)) {
+    auto one = [](float z, float base) {  // times exp(-base)
+      return z > -INFINITY ? exp_fast(fminf(z, 0.0f) - base) * rcp(1.0f + exp_fast(-fabsf(z))) : 0.0f;
+    };
+    auto other = [](float z) {
+      const float t = exp_fast(-fabsf(z)), r = rcp(1.0f + t);
+      return z < 0.0f ? r : t * r;
+    };
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      again(q);
+      shut(v[q], status);
+      const float base = fminf(group_max<SUB>(lane_max(v[q])), 0.0f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if constexpr (REST) rest[q][i] = F2(other(v[q][i].x()), other(v[q][i].y()));
+        v[q][i] = F2(one(v[q][i].x(), base), one(v[q][i].y(), base));
+      }
+      sum[q] = sum_and_dot<SUB>(v[q], D, dot);
     }
-    sum = group_sum<SUB>(s);
   }
 }
 
@@ -255,43 +361,115 @@ __device__ __forceinline__ int find_sequence(const int32_t* off, int B, int t) {
   return lo;
 }
 
-// The slots of a group's token: how many name an expert.  They are counted in `hist` if there is one.
-template <int SUB>
-__device__ __forceinline__ int routed_slots(const int32_t* idx, int t, int k, int E, int j, bool live,
-                                            int* hist, uint32_t* status) {
+// The same for one t of a whole warp: 32 bounds at a time.  `bound`: first_bound(), loaded ahead.
+__device__ __forceinline__ int first_bound(const int32_t* off, int B, int lane) {
+  const int i = lane * ((B + 31) >> 5);
+  return i < B ? __ldg(off + i) : INT_MAX;
+}
+__device__ __forceinline__ int find_sequence_warp(const int32_t* off, int B, int t, int lane, int bound) {
+  int lo = 0, n = B;
+  while (true) {
+    const int step = (n + 31) >> 5;
+    const unsigned le = __ballot_sync(kFull, bound <= t && lane * step < n);
+    const int c = le ? 31 - __clz(le) : 0;
+    lo += c * step;
+    n = min(step, n - c * step);
+    if (n <= 1) return lo;
+    const int i = lane * ((n + 31) >> 5);
+    bound = i < n ? __ldg(off + lo + i) : INT_MAX;
+  }
+}
+
+// How many slots of token t name an expert; each is counted in `hist` if there is one.
+__device__ __forceinline__ int routed_slots(const int32_t* idx, int t, int k, int E, int* hist, uint32_t* status) {
+  const int32_t* mine = idx + (size_t)t * k;
   int n = 0;
-  for (int q = 0; q < k; q += SUB) {
-    int e = -1;
-    if (live && q + j < k) e = __ldg(idx + (size_t)t * k + q + j);
-    if (e >= E) {
-      raise_status(status, LRMOE_ST_BAD_EXPERT);
-      e = -1;
+  for (int first = 0; first < k; first += 4) {
+    int e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = first + i < k ? __ldg(mine + first + i) : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e[i] >= E) {
+        raise_status(status, LRMOE_ST_BAD_EXPERT);
+      } else if (e[i] >= 0) {
+        if (hist != nullptr) atomicAdd(hist + e[i], 1);
+        ++n;
+      }
     }
-    if (hist != nullptr && e >= 0) atomicAdd(hist + e, 1);
-    const unsigned set = __ballot_sync(kFull, e >= 0);
-    if constexpr (SUB == 32)
-      n += __popc(set);
-    else
-      n += __popc((set >> (threadIdx.x & 31 & ~(SUB - 1))) & ((1u << SUB) - 1u));
   }
   return n;
 }
 
-template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, bool VEC>
-__global__ void __launch_bounds__(kThreads) balance_kernel(const BalanceParams p) {
+__device__ __forceinline__ RowSums operator+(const RowSums& a, const RowSums& b) {
+  return RowSums{a.tokens + b.tokens, a.pairs + b.pairs, a.z + b.z, 0};
+}
+
+__device__ __forceinline__ RowSums warp_sum(RowSums r) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1)
+    r = r + RowSums{__shfl_xor_sync(kFull, r.tokens, o), __shfl_xor_sync(kFull, r.pairs, o),
+                    __shfl_xor_sync(kFull, r.z, o), 0};
+  return r;
+}
+
+// Tokens of a group in flight in the sums, besides those that are being read.
+template <lrmoe_dtype DT, int VPL, int G>
+constexpr int at_once() {
+  return DT == LRMOE_BF16 && VPL == 8 && G > 1 ? 2 : 1;
+}
+
+constexpr int kChunk = 512;  // tokens whose slots a block looks at at a time
+
+// Threads of a run: as many as have registers for their values.
+constexpr int run_threads(int vpl) { return 4096 / vpl; }
+constexpr int values_of(int E) { return E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+constexpr int lanes_of(int E) { return E <= 32 ? 4 : E <= 64 ? 8 : E <= 128 ? 16 : 32; }
+
+template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, int G>
+__global__ void __launch_bounds__(run_threads(VPL), 2) balance_kernel(const BalanceParams p) {
   constexpr int TPW = 32 / SUB;  // tokens of a warp at a time
-  using R = Row<DT, VPL, SUB, VEC>;
-  extern __shared__ float smem[];  // [kWarps][E] sums, [E] counts
+  constexpr int U = at_once<DT, VPL, G>();
+  constexpr int N = VPL / 2;
+  constexpr int THREADS = run_threads(VPL), WARPS = THREADS / 32;
+  using R = Row<DT, VPL, SUB, G>;
+  extern __shared__ float smem[];  // [WARPS][E] sums, [E] counts
   const int E = p.E;
-  int* hist = reinterpret_cast<int*>(smem + (size_t)kWarps * E);
-  __shared__ RowSums warp_sums[kWarps];
+  int* hist = reinterpret_cast<int*>(smem + (size_t)WARPS * E);
+  __shared__ RowSums warp_sums[32];
+  __shared__ bool routed[kChunk];
+  const char* logits = static_cast<const char*>(p.logits);
+  const size_t step = (size_t)TPW * E * R::kSize;  // to a warp's next tokens
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / SUB, j = lane % SUB;
-  for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
+  if (threadIdx.x < 32) warp_sums[threadIdx.x] = RowSums{0, 0, 0.0f, 0};
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0u;
   const int t0 = blockIdx.x * p.run, t1 = min(p.T, t0 + p.run);
-  int b = p.off ? find_sequence(p.off, p.B, t0) : 0;
+  int b = 0, at = t0;
+  int bound = 0;
+  if (p.off) {
+    bound = first_bound(p.off, p.B, lane);
+    at = max(t0, __ldg(p.off));
+  }
+  // A warp's first tokens from `at` on are fetched before it is known which sequence they are of; marks tell
+  // later which count.
+  typename R::Raw raw[U];
+  int first;
+  const char* from;
+  auto fetch = [&](int q, const char* place, int t, int end, typename R::Raw& r) {
+    const bool live = t < end;
+    R::fetch(place + q * step, E, j, live, live ? R::masked() : 0u, r);
+  };
+  auto begin = [&]() {
+    first = at + warp * (TPW * U);
+    from = logits + R::place(first + sub, E, j);
+#pragma unroll
+    for (int q = 0; q < U; ++q) fetch(q, from, first + q * TPW + sub, t1, raw[q]);
+  };
+  begin();
+  if (p.off) b = find_sequence_warp(p.off, p.B, t0, lane, bound);
   for (; b < p.B; ++b) {
     int lo = 0, hi = p.T;
     if (p.off) {
@@ -302,94 +480,118 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(const BalanceParams p
     lo = max(lo, t0);
     hi = min(hi, t1);
     if (lo >= hi) continue;
-    float col[VPL];
+    F2 col[N];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) col[i] = 0.0f;
+    for (int i = 0; i < N; ++i) col[i] = F2(0.0f);
     int tokens = 0, pairs = 0;
     float zz = 0.0f;
     __syncthreads();  // the counts are 0
-    for (int first = lo + warp * TPW; first < hi; first += kWarps * TPW) {
-      const int t = first + sub;
-      const bool live = t < hi;
-      float v[VPL], u[VPL], sum, zmax;
-      R::load(p.logits, (size_t)t * E, E, j, live, live ? -INFINITY : 0.0f, v);
-      const int n = routed_slots<SUB>(p.idx, t, p.k, E, j, live, hist, p.status);
-      if constexpr (SIGMOID) {
-        sigmoid_terms<VPL, SUB>(v, u, sum, p.status);
-      } else {
-        softmax_terms<VPL, SUB>(v, u, sum, zmax, p.status);
+    for (int c0 = lo; c0 < hi; c0 += kChunk) {
+      const int c1 = min(hi, c0 + kChunk);
+      if (c0 != at) {
+        at = c0;
+        begin();
       }
-      const float inv = n > 0 && sum > 0.0f ? rcp(sum) : 0.0f;
+      if (c0 != lo) __syncthreads();  // all have read their tokens' marks
+      for (int i = threadIdx.x; i < kChunk; i += THREADS) {
+        const int n = c0 + i < c1 ? routed_slots(p.idx, c0 + i, p.k, E, hist, p.status) : 0;
+        routed[i] = n > 0;
+        tokens += n > 0;
+        pairs += n;
+      }
+      __syncthreads();
+      for (; first < c1; first += WARPS * TPW * U) {
+        F2 v[U][N];
+        float sum[U], zmax[U];
+        bool in[U];
+        auto again = [&](int q) {
+          typename R::Raw r;
+          fetch(q, from, first + q * TPW + sub, c1, r);
+          R::unpack(r, v[q]);
+        };
+        const char* ahead = from + WARPS * U * step;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) col[i] = fmaf(u[i], inv, col[i]);
-      if (p.z_coef != 0.0f) {
-        if constexpr (SIGMOID) softmax_terms<VPL, SUB>(v, u, sum, zmax, p.status);
-        const float lse = sum > 0.0f ? zmax + logf(sum) : 0.0f;
-        if (n > 0) zz = fmaf(lse, lse, zz);
+        for (int q = 0; q < U; ++q) {
+          R::unpack(raw[q], v[q]);
+          in[q] = routed[first - c0 + q * TPW + sub];
+          fetch(q, ahead, first + (WARPS * U + q) * TPW + sub, c1, raw[q]);
+        }
+        if constexpr (SIGMOID) {
+          F2 unused[1][N];
+          sigmoid_terms<false, N, SUB, U>(v, unused, sum, p.status, again);
+        } else {
+          softmax_terms<N, SUB, U>(v, sum, zmax, p.status, again);
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          const F2 inv(in[q] && sum[q] > 0.0f ? rcp(sum[q]) : 0.0f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) col[i] = fma2(v[q][i], inv, col[i]);
+        }
+        if (p.z_coef != 0.0f) {
+          if constexpr (SIGMOID) {
+#pragma unroll
+            for (int q = 0; q < U; ++q) again(q);
+            softmax_terms<N, SUB, U>(v, sum, zmax, p.status, again);
+          }
+#pragma unroll
+          for (int q = 0; q < U; ++q) {
+            const float lse = sum[q] > 0.0f ? zmax[q] + log_fast(sum[q]) : 0.0f;
+            if (in[q]) zz = fmaf(lse, lse, zz);
+          }
+        }
+        from = ahead;
       }
-      tokens += n > 0;
-      pairs += n;
+      at = c1;
+      begin();
     }
 #pragma unroll
     for (int o = SUB; o < 32; o <<= 1) {  // the warp's groups
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) col[i] += __shfl_xor_sync(kFull, col[i], o);
-      tokens += __shfl_xor_sync(kFull, tokens, o);
-      pairs += __shfl_xor_sync(kFull, pairs, o);
+      for (int i = 0; i < N; ++i)
+        col[i] = col[i] + F2(__shfl_xor_sync(kFull, col[i].x(), o), __shfl_xor_sync(kFull, col[i].y(), o));
       zz += __shfl_xor_sync(kFull, zz, o);
     }
     if (sub == 0) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (R::at(i, j) < E) smem[(size_t)warp * E + R::at(i, j)] = col[i];
+      for (int i = 0; i < N; ++i) {
+        if (R::at(2 * i, j) < E) smem[(size_t)warp * E + R::at(2 * i, j)] = col[i].x();
+        if (R::at(2 * i + 1, j) < E) smem[(size_t)warp * E + R::at(2 * i + 1, j)] = col[i].y();
+      }
     }
+    tokens = __reduce_add_sync(kFull, tokens);
+    pairs = __reduce_add_sync(kFull, pairs);
     if (lane == 0) warp_sums[warp] = RowSums{tokens, pairs, zz, 0};
     __syncthreads();
     const size_t row = (size_t)blockIdx.x + b;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
+    for (int e = threadIdx.x; e < E; e += THREADS) {
       float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += smem[(size_t)w * E + e];
+#pragma unroll 8
+      for (int w = 0; w < WARPS; ++w) s += smem[(size_t)w * E + e];
       p.sums[row * E + e] = s;
       p.hist[row * E + e] = hist[e];
       hist[e] = 0;
     }
-    if (threadIdx.x == 0) {
-      RowSums r{0, 0, 0.0f, 0};
-      for (int w = 0; w < kWarps; ++w) {
-        r.tokens += warp_sums[w].tokens;
-        r.pairs += warp_sums[w].pairs;
-        r.z += warp_sums[w].z;
-      }
-      p.rows[row] = r;
+    if (warp == WARPS - 1) {  // one of those with the fewest columns above
+      const RowSums r = warp_sum(warp_sums[lane]);
+      if (lane == 0) p.rows[row] = r;
     }
   }
 }
 
-template <typename V>
-__device__ __forceinline__ V block_sum(V v, V* scratch /* [kWarps + 1] */) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  V s = scratch[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) s += scratch[w];
-  return s;
-}
-
 // One block to COLS experts of a sequence: its pieces' rows are added in order.
-template <int COLS>
-__global__ void __launch_bounds__(kThreads) balance_sum_kernel(const BalanceParams p) {
-  constexpr int ROWS = kThreads / COLS;  // rows at a time
+template <int COLS, int THREADS>
+__global__ void __launch_bounds__(THREADS) balance_sum_kernel(const BalanceParams p) {
+  constexpr int ROWS = THREADS / COLS, WARPS = THREADS / 32;
+  constexpr int AHEAD = COLS == 32 ? 10 : 8;  // rows of a thread in flight: all of a single sequence's
   const int E = p.E;
   const int b = blockIdx.x / p.col_blocks, cb = blockIdx.x - b * p.col_blocks;
   const int c = threadIdx.x % COLS, r = threadIdx.x / COLS, e = cb * COLS + c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ float fsum[ROWS][COLS];
   __shared__ int isum[ROWS][COLS];
-  __shared__ float fs[kWarps + 1];
-  __shared__ int is[kWarps + 1];
+  __shared__ RowSums warps[WARPS];
+  __shared__ float dots[WARPS];
   __shared__ bool last;
   pdl_wait();
   pdl_trigger();
@@ -404,196 +606,261 @@ __global__ void __launch_bounds__(kThreads) balance_sum_kernel(const BalancePara
     }
   }
   const int first = lo / p.run + b, rows = hi > lo ? (hi - 1) / p.run - lo / p.run + 1 : 0;
+  RowSums all{0, 0, 0.0f, 0};
+  for (int i = threadIdx.x; i < rows; i += THREADS) all = all + p.rows[first + i];
   float s = 0.0f;
   int n = 0;
-  if (e < E) {
-#pragma unroll 4
-    for (int i = r; i < rows; i += ROWS) {
-      s += p.sums[(size_t)(first + i) * E + e];
-      n += p.hist[(size_t)(first + i) * E + e];
+  const size_t base = (size_t)first * E + e;
+  for (int at = r; at < rows; at += AHEAD * ROWS) {
+    float x[AHEAD];
+    int y[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const bool on = at + i * ROWS < rows && e < E;
+      const size_t place = base + (size_t)(at + i * ROWS) * E;
+      x[i] = on ? p.sums[place] : 0.0f;
+      y[i] = on ? p.hist[place] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      s += x[i];
+      n += y[i];
     }
   }
   fsum[r][c] = s;
   isum[r][c] = n;
-  int tokens = 0, pairs = 0;
-  float z = 0.0f;
-  for (int i = threadIdx.x; i < rows; i += kThreads) {
-    const RowSums q = p.rows[first + i];
-    tokens += q.tokens;
-    pairs += q.pairs;
-    z += q.z;
-  }
-  tokens = block_sum(tokens, is);
-  pairs = block_sum(pairs, is);
-  z = block_sum(z, fs);
-  float dot = 0.0f;
-  if (r == 0 && e < E) {
-    for (int i = 1; i < ROWS; ++i) {
-      s += fsum[i][c];
-      n += isum[i][c];
+  all = warp_sum(all);
+  if (lane == 0) warps[warp] = all;
+  __syncthreads();
+  if (threadIdx.x < COLS) {
+    all = warp_sum(lane < WARPS ? warps[lane] : RowSums{0, 0, 0.0f, 0});
+    float dot = 0.0f;
+    if (e < E) {
+      s = fsum[0][c];
+      n = isum[0][c];
+#pragma unroll
+      for (int i = 1; i < ROWS; ++i) {
+        s += fsum[i][c];
+        n += isum[i][c];
+      }
+      p.counts[(size_t)b * E + e] = n;
+      p.mean[(size_t)b * E + e] = all.tokens > 0 ? s / (float)all.tokens : 0.0f;
+      dot = (float)n * s;
     }
-    p.counts[(size_t)b * E + e] = n;
-    p.mean[(size_t)b * E + e] = tokens > 0 ? s / (float)tokens : 0.0f;
-    dot = (float)n * s;
+    dot = group_sum<32>(dot);
+    if (lane == 0) dots[warp] = dot;
   }
-  dot = block_sum(dot, fs);
+  __syncthreads();
   if (threadIdx.x == 0) {
-    p.part[blockIdx.x] = pairs > 0 ? dot * ((float)E / ((float)pairs * (float)tokens)) : 0.0f;
+    float dot = dots[0];
+#pragma unroll
+    for (int w = 1; w < COLS / 32; ++w) dot += dots[w];
+    dot = all.pairs > 0 ? dot * ((float)E / ((float)all.pairs * (float)all.tokens)) : 0.0f;
     if (cb == 0) {
-      p.stats[2 * b] = tokens;
-      p.stats[2 * b + 1] = pairs;
-      p.part[(size_t)p.B * p.col_blocks + b] = z;
+      p.stats[2 * b] = all.tokens;
+      p.stats[2 * b + 1] = all.pairs;
     }
-    __threadfence();
-    last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
-    __threadfence();
+    if (gridDim.x == 1) {
+      p.stats[2] = all.tokens;
+      p.stats[3] = all.tokens > 0;
+      p.loss[0] = p.coef * dot;
+      p.loss[1] = all.tokens > 0 ? p.z_coef * (all.z / (float)all.tokens) : 0.0f;
+    } else {
+      p.part[blockIdx.x] = dot;
+      if (cb == 0) p.part[(size_t)p.B * p.col_blocks + b] = all.z;
+      unsigned before;  // releases this block's parts and acquires the others'
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.ticket) : "memory");
+      last = before == gridDim.x - 1;
+    }
   }
+  if (gridDim.x == 1) return;
   __syncthreads();
   if (!last) return;
   // the last block: every other's part is written
   const volatile float* part = p.part;
   const volatile int32_t* stats = p.stats;
   float l = 0.0f;
-  z = 0.0f;
-  int all = 0, live = 0;
-  for (long long i = threadIdx.x; i < (long long)p.B * p.col_blocks; i += kThreads) l += part[i];
-  for (int i = threadIdx.x; i < p.B; i += kThreads) {
-    z += part[(size_t)p.B * p.col_blocks + i];
-    all += stats[2 * i];
-    live += stats[2 * i] > 0;
+  all = RowSums{0, 0, 0.0f, 0};  // all tokens and the sequences that have any
+  for (long long i = threadIdx.x; i < (long long)p.B * p.col_blocks; i += THREADS) l += part[i];
+  for (int i = threadIdx.x; i < p.B; i += THREADS) {
+    const int t = stats[2 * i];
+    all = all + RowSums{t, t > 0, part[(size_t)p.B * p.col_blocks + i], 0};
   }
-  l = block_sum(l, fs);
-  z = block_sum(z, fs);
-  all = block_sum(all, is);
-  live = block_sum(live, is);
-  if (threadIdx.x == 0) {
-    p.stats[2 * p.B] = all;
-    p.stats[2 * p.B + 1] = live;
-    p.loss[0] = live > 0 ? p.coef * (l / (float)live) : 0.0f;
-    p.loss[1] = all > 0 ? p.z_coef * (z / (float)all) : 0.0f;
+  l = group_sum<32>(l);
+  all = warp_sum(all);
+  if (lane == 0) {
+    dots[warp] = l;
+    warps[warp] = all;
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  l = group_sum<32>(lane < WARPS ? dots[lane] : 0.0f);
+  all = warp_sum(lane < WARPS ? warps[lane] : RowSums{0, 0, 0.0f, 0});
+  if (lane == 0) {
+    p.stats[2 * p.B] = all.tokens;
+    p.stats[2 * p.B + 1] = all.pairs;
+    p.loss[0] = all.pairs > 0 ? p.coef * (l / (float)all.pairs) : 0.0f;
+    p.loss[1] = all.tokens > 0 ? p.z_coef * (all.z / (float)all.tokens) : 0.0f;
   }
 }
 
-template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, bool VEC>
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const BalanceGradParams p) {
+// Blocks of the gradient to an SM: few, so that each warp's start (its sequence's factors, its first row) is paid
+// for by many tokens (T = 32749, E = 250, 16-bit sigmoids: 4, 3 and 2 blocks take 16.8, 13.9 and 13.6 us).
+constexpr int grad_blocks(int vpl) { return vpl > 8 ? 1 : 2; }
+
+template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, int G>
+__global__ void __launch_bounds__(kThreads, grad_blocks(VPL))
+    balance_grad_kernel(const BalanceGradParams p) {
   constexpr int TPW = 32 / SUB;
-  using R = Row<DT, VPL, SUB, VEC>;
+  constexpr int N = VPL / 2;
+  using R = Row<DT, VPL, SUB, G>;
   const int lane = threadIdx.x & 31, sub = lane / SUB, j = lane % SUB;
   const int E = p.E;
   pdl_wait();
   pdl_trigger();
+  // a warp's tokens lie side by side, so that its sequence seldom changes
+  const long long w0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.each;
+  if (w0 >= p.T) return;
+  const int end = (int)min((long long)p.T, w0 + p.each);
+  const size_t step = (size_t)TPW * E * R::kSize, start = R::place(w0 + sub, E, j);
+  const char* from = static_cast<const char*>(p.logits) + start;
+  const char* plus = p.add ? static_cast<const char*>(p.add) + start : nullptr;
+  char* to = static_cast<char*>(p.dlogits) + start;
+  auto fetch = [&](const char* at, bool on, typename R::Raw& r) { R::fetch(at, E, j, on, on ? R::masked() : 0u, r); };
+  typename R::Raw raw, add;
+  fetch(from, (int)w0 + sub < end, raw);
+  if (plus) R::fetch(plus, E, j, (int)w0 + sub < end, 0u, add);
+  const int bound = p.off ? first_bound(p.off, p.B, lane) : 0;
   const int all = __ldg(p.stats + 2 * p.B), live_seqs = __ldg(p.stats + 2 * p.B + 1);
   const float d0 = p.dloss ? __ldg(p.dloss) : 1.0f, d1 = p.dloss ? __ldg(p.dloss + 1) : 1.0f;
+  // what rows before the first sequence and behind the last one hold does not matter
+  const int in_lo = p.off ? __ldg(p.off) : 0, in_hi = p.off ? min(end, __ldg(p.off + p.B)) : end;
+  auto inside = [&](int t) { return t >= in_lo && t < in_hi; };
+  // bit i: token first + i of the next 32 has a slot that names an expert
+  auto marks = [&](int first) {
+    const int t = first + lane;
+    return __ballot_sync(kFull, inside(t) && routed_slots(p.idx, t, p.k, E, nullptr, p.status) > 0);
+  };
+  unsigned routed = marks((int)w0);
   const float c0 = live_seqs > 0 ? p.coef * d0 * (float)E / (float)live_seqs : 0.0f;
   const float cz = all > 0 ? 2.0f * p.z_coef * d1 / (float)all : 0.0f;
-  // a warp's tokens lie side by side, so that its sequence seldom changes
-  const long long warps = (long long)gridDim.x * kWarps;
-  const long long each = ((p.T + warps - 1) / warps + TPW - 1) / TPW * TPW;
-  const long long w0 = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * each;
-  const int end = (int)min((long long)p.T, w0 + each);
-  int seq = -1, seq_lo = 0, seq_hi = 0;  // the sequence whose factors are in D
-  float D[VPL];
+  int seq = p.off ? find_sequence_warp(p.off, p.B, (int)w0, lane, bound) : 0;
+  int seq_lo = 0, seq_hi = p.T;
+  F2 D[N];  // of sequence `seq`
+  auto factors = [&]() {
+    if (p.off) {
+      seq_lo = __ldg(p.off + seq);
+      seq_hi = __ldg(p.off + seq + 1);
+    }
+    const float nm = (float)__ldg(p.stats + 2 * seq) * (float)__ldg(p.stats + 2 * seq + 1);
+    const float f = nm > 0.0f ? c0 / nm : 0.0f;
+    auto one = [&](int e) { return e < E ? f * (float)__ldg(p.counts + (size_t)seq * E + e) : 0.0f; };
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) D[i] = 0.0f;
+    for (int i = 0; i < N; ++i) D[i] = F2(one(R::at(2 * i, j)), one(R::at(2 * i + 1, j)));
+  };
+  factors();
   for (long long first = w0; first < end; first += TPW) {
     const int t = (int)first + sub;
-    const bool live = t < end;
-    const size_t row = (size_t)t * E;
-    if (live && (seq < 0 || t < seq_lo || t >= seq_hi)) {
-      seq = p.off ? find_sequence(p.off, p.B, t) : 0;
-      seq_lo = p.off ? __ldg(p.off + seq) : 0;
-      seq_hi = p.off ? __ldg(p.off + seq + 1) : p.T;
-      const float nm = (float)__ldg(p.stats + 2 * seq) * (float)__ldg(p.stats + 2 * seq + 1);
-      const float f = nm > 0.0f ? c0 / nm : 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        D[i] = R::at(i, j) < E ? f * (float)__ldg(p.counts + (size_t)seq * E + R::at(i, j)) : 0.0f;
+    F2 v[1][N], rest[1][N];
+    float sum[1], zmax[1];
+    auto again = [&](int) {
+      typename R::Raw r;
+      fetch(from, inside(t), r);
+      R::unpack(r, v[0]);
+    };
+    R::unpack(raw, v[0]);
+    F2 d[N];
+    if (plus) R::unpack(add, d);
+    fetch(from + step, t + TPW < end, raw);
+    if (plus) {
+      plus += step;
+      R::fetch(plus, E, j, t + TPW < end, 0u, add);
     }
-    // rows behind the last sequence are not read
-    const bool inside = live && t >= seq_lo && t < seq_hi;
-    float v[VPL], u[VPL], sum, zmax;
-    R::load(p.logits, row, E, j, inside, inside ? -INFINITY : 0.0f, v);
-    const bool counts = routed_slots<SUB>(p.idx, t, p.k, E, j, inside, nullptr, p.status) > 0;
-    float dz[VPL];
+    const int place = (int)(first - w0) % 32;
+    if (place == 0 && first != w0) routed = marks((int)first);
+    const bool in = (routed >> (place + sub)) & 1u;
+    float dot;
+    if constexpr (SIGMOID)
+      sigmoid_terms<true, N, SUB, 1>(v, rest, sum, p.status, again, &D, &dot);
+    else
+      softmax_terms<N, SUB, 1>(v, sum, zmax, p.status, again, &D, &dot);
+    const bool moved = p.off && in && (t < seq_lo || t >= seq_hi);
+    if (moved) {
+      seq = find_sequence(p.off, p.B, t);
+      factors();
+    }
+    if (__any_sync(kFull, moved)) dot = group_sum<SUB>(lane_dot(v[0], D));
+    const float inv = in && sum[0] > 0.0f ? rcp(sum[0]) : 0.0f;
+    dot *= inv;
+    if constexpr (!SIGMOID)
+      if (p.z_coef != 0.0f && inv > 0.0f) dot -= cz * (zmax[0] + log_fast(sum[0]));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      F2 x = v[0][i] * F2(inv);
+      if constexpr (SIGMOID) x = x * rest[0][i];
+      const F2 y = D[i] + F2(-dot);
+      d[i] = plus ? fma2(x, y, d[i]) : x * y;
+    }
     if constexpr (SIGMOID) {
-      sigmoid_terms<VPL, SUB>(v, u, sum, p.status);
-      const float inv = counts && sum > 0.0f ? rcp(sum) : 0.0f;
-      float dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) dot = fmaf(D[i], u[i], dot);
-      dot = group_sum<SUB>(dot) * inv;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const float t1 = exp_neg(-fabsf(v[i]));
-        const float r = rcp(1.0f + t1);
-        dz[i] = u[i] * inv * (D[i] - dot) * (v[i] >= 0.0f ? t1 * r : r);
-      }
       if (p.z_coef != 0.0f) {
-        softmax_terms<VPL, SUB>(v, u, sum, zmax, p.status);
-        const float w = counts && sum > 0.0f ? cz * (zmax + logf(sum)) * rcp(sum) : 0.0f;
+        again(0);
+        softmax_terms<N, SUB, 1>(v, sum, zmax, p.status, again);
+        const F2 w(in && sum[0] > 0.0f ? cz * (zmax[0] + log_fast(sum[0])) * rcp(sum[0]) : 0.0f);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) dz[i] = fmaf(w, u[i], dz[i]);
+        for (int i = 0; i < N; ++i) d[i] = fma2(w, v[0][i], d[i]);
       }
-    } else {
-      softmax_terms<VPL, SUB>(v, u, sum, zmax, p.status);
-      const float inv = counts && sum > 0.0f ? rcp(sum) : 0.0f;
-      float dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) dot = fmaf(D[i], u[i], dot);
-      dot = group_sum<SUB>(dot) * inv;
-      if (p.z_coef != 0.0f && inv > 0.0f) dot -= cz * (zmax + logf(sum));
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) dz[i] = u[i] * inv * (D[i] - dot);
     }
-    if (p.add) {
-      R::load(p.add, row, E, j, live, 0.0f, v);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) dz[i] += v[i];
-    }
-    if (live) R::store(p.dlogits, row, E, j, dz);
+    R::store(to, E, j, t < end, d);
+    from += step;
+    to += step;
   }
 }
 
-// Lanes and values of a token by the number of experts; rows of whole 16-byte vectors or not.
-template <template <lrmoe_dtype, bool, int, int, bool> class F, lrmoe_dtype DT, bool SIGMOID, bool VEC,
-          typename P>
+// Lanes and values of a token by the number of experts.
+template <template <lrmoe_dtype, bool, int, int, int> class F, lrmoe_dtype DT, bool SIGMOID, int G, typename P>
 cudaError_t by_width(const P& p, cudaStream_t s) {
-  if (p.E <= 32) return F<DT, SIGMOID, 8, 4, VEC>::run(p, s);
-  if (p.E <= 64) return F<DT, SIGMOID, 8, 8, VEC>::run(p, s);
-  if (p.E <= 128) return F<DT, SIGMOID, 8, 16, VEC>::run(p, s);
-  if (p.E <= 256) return F<DT, SIGMOID, 8, 32, VEC>::run(p, s);
-  if (p.E <= 512) return F<DT, SIGMOID, 16, 32, VEC>::run(p, s);
-  return F<DT, SIGMOID, 32, 32, VEC>::run(p, s);
+  if (p.E <= 32) return F<DT, SIGMOID, 8, 4, G>::run(p, s);
+  if (p.E <= 64) return F<DT, SIGMOID, 8, 8, G>::run(p, s);
+  if (p.E <= 128) return F<DT, SIGMOID, 8, 16, G>::run(p, s);
+  if (p.E <= 256) return F<DT, SIGMOID, 8, 32, G>::run(p, s);
+  if (p.E <= 512) return F<DT, SIGMOID, 16, 32, G>::run(p, s);
+  return F<DT, SIGMOID, 32, 32, G>::run(p, s);
 }
 
-template <template <lrmoe_dtype, bool, int, int, bool> class F, typename P>
-cudaError_t by_type(const P& p, lrmoe_dtype dt, bool sigmoid, cudaStream_t s) {
+// 16-byte vectors where rows are whole ones, else pairs of 16-bit values, else single values.
+template <template <lrmoe_dtype, bool, int, int, int> class F, bool SIGMOID, typename P>
+cudaError_t by_vector(const P& p, lrmoe_dtype dt, cudaStream_t s) {
   if (dt == LRMOE_BF16) {
-    if (p.E % 8 == 0)
-      return sigmoid ? by_width<F, LRMOE_BF16, true, true>(p, s) : by_width<F, LRMOE_BF16, false, true>(p, s);
-    return sigmoid ? by_width<F, LRMOE_BF16, true, false>(p, s) : by_width<F, LRMOE_BF16, false, false>(p, s);
+    if (p.E % 8 == 0) return by_width<F, LRMOE_BF16, SIGMOID, 8>(p, s);
+    if (p.E % 2 == 0) return by_width<F, LRMOE_BF16, SIGMOID, 2>(p, s);
+    return by_width<F, LRMOE_BF16, SIGMOID, 1>(p, s);
   }
-  if (p.E % 4 == 0)
-    return sigmoid ? by_width<F, LRMOE_F32, true, true>(p, s) : by_width<F, LRMOE_F32, false, true>(p, s);
-  return sigmoid ? by_width<F, LRMOE_F32, true, false>(p, s) : by_width<F, LRMOE_F32, false, false>(p, s);
+  if (p.E % 4 == 0) return by_width<F, LRMOE_F32, SIGMOID, 4>(p, s);
+  return by_width<F, LRMOE_F32, SIGMOID, 1>(p, s);
 }
 
-template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, bool VEC>
+template <template <lrmoe_dtype, bool, int, int, int> class F, typename P>
+cudaError_t by_type(const P& p, lrmoe_dtype dt, bool sigmoid, cudaStream_t s) {
+  return sigmoid ? by_vector<F, true>(p, dt, s) : by_vector<F, false>(p, dt, s);
+}
+
+template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, int G>
 struct Forward {
   static cudaError_t run(const BalanceParams& p, cudaStream_t s) {
-    return launch_pdl(balance_kernel<DT, SIGMOID, VPL, SUB, VEC>, dim3(p.runs), dim3(kThreads),
-                      sizeof(float) * (kWarps + 1) * (size_t)p.E, s, p);
+    const size_t smem = sizeof(float) * (run_threads(VPL) / 32 + 1) * (size_t)p.E;  // 36 KB at most
+    return launch_pdl(balance_kernel<DT, SIGMOID, VPL, SUB, G>, dim3(p.runs), dim3(run_threads(VPL)), smem, s, p);
   }
 };
 
-template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, bool VEC>
+template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, int G>
 struct Backward {
-  static cudaError_t run(const BalanceGradParams& p, cudaStream_t s) {
-    const long long per = kWarps * (32 / SUB);
-    long long blocks = (p.T + per - 1) / per;
-    const long long cap = (long long)num_sms() * 8;
-    if (blocks > cap) blocks = cap;
-    return launch_pdl(balance_grad_kernel<DT, SIGMOID, VPL, SUB, VEC>, dim3((unsigned)blocks),
+  static cudaError_t run(const BalanceGradParams& given, cudaStream_t s) {
+    BalanceGradParams p = given;
+    constexpr int TPW = 32 / SUB;
+    const long long warps = (long long)num_sms() * grad_blocks(VPL) * kWarps;
+    p.each = (int)(((p.T + warps - 1) / warps + TPW - 1) / TPW * TPW);
+    const long long per = (long long)p.each * kWarps;
+    return launch_pdl(balance_grad_kernel<DT, SIGMOID, VPL, SUB, G>, dim3((unsigned)((p.T + per - 1) / per)),
                       dim3(kThreads), 0, s, p);
   }
 };
@@ -605,13 +872,16 @@ struct Plan {  // what the sizes alone fix
 
 Plan plan_of(int T, int E, int B) {
   Plan q;
-  // runs of at least a block's tokens at a time
-  const int sub = E <= 32 ? 4 : E <= 64 ? 8 : E <= 128 ? 16 : 32;
-  const int at_a_time = kWarps * (32 / sub);
+  // Runs of at least a block's tokens at a time, and of four times as many where that leaves 16 runs: the rows are
+  // then few enough for one block to add them up (T = 16384, E = 128: 128 runs take 9.5 us, 293 runs 10.7 us).
+  const int at_a_time = run_threads(values_of(E)) / lanes_of(E);
   q.run = (T + kMaxRuns - 1) / kMaxRuns;
-  if (q.run < at_a_time) q.run = at_a_time;
+  const int least = min(4, (T + 16 * at_a_time - 1) / (16 * at_a_time)) * at_a_time;
+  if (q.run < least) q.run = least;
   q.runs = (int)(((long long)T + q.run - 1) / q.run);
-  q.cols = B >= 64 ? 64 : 8;
+  // Columns of a block that adds rows up.  Few rows are one block's, which then needs no ticket; a single sequence
+  // of many runs is split further, and many sequences have few rows each.
+  q.cols = B >= 8 ? 64 : q.runs <= 148 ? 128 : 32;
   q.col_blocks = (E + q.cols - 1) / q.cols;
   auto up = [](size_t n) { return (n + 15) & ~size_t(15); };
   const size_t pieces = (size_t)q.runs + B;
@@ -659,8 +929,9 @@ cudaError_t launch_balance(const void* logits, int T, int E, lrmoe_dtype dt, con
   cudaError_t e = by_type<Forward>(p, dt, fn == LRMOE_SCORE_SIGMOID, s);
   if (e != cudaSuccess) return e;
   const unsigned blocks = (unsigned)((long long)B * q.col_blocks);
-  auto kern = q.cols == 64 ? balance_sum_kernel<64> : balance_sum_kernel<8>;
-  return launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, s, p);
+  if (q.cols == 64) return launch_pdl(balance_sum_kernel<64, 256>, dim3(blocks), dim3(256), 0, s, p);
+  if (q.cols == 32) return launch_pdl(balance_sum_kernel<32, 1024>, dim3(blocks), dim3(1024), 0, s, p);
+  return launch_pdl(balance_sum_kernel<128, 1024>, dim3(blocks), dim3(1024), 0, s, p);
 }
 
 cudaError_t launch_balance_grad(const void* logits, int T, int E, lrmoe_dtype dt,
@@ -668,7 +939,7 @@ cudaError_t launch_balance_grad(const void* logits, int T, int E, lrmoe_dtype dt
                                 int B, float coef, float z_coef, const int32_t* counts,
                                 const int32_t* stats, const float* dloss, const void* add,
                                 void* dlogits, uint32_t* status, cudaStream_t s) {
-  const BalanceGradParams p{logits, idx,   off,   T,     E,   k,       B,
+  const BalanceGradParams p{logits, idx,    off,    T,     E,     k,   B,       0,
                             coef,   z_coef, counts, stats, dloss, add, dlogits, status};
   return by_type<Backward>(p, dt, fn == LRMOE_SCORE_SIGMOID, s);
 }
