@@ -11,14 +11,15 @@
 // The piece of run c in sequence b writes its sums over tokens to row c + b of the workspace: along
 // the batch each piece raises c or b or both, so that no two pieces share a row and a sequence's rows
 // lie side by side.  A second kernel adds each sequence's rows in order (no atomics on floats: the
-// same inputs give the same bits) and its last block adds the losses up.
+// same inputs give the same bits) and its last block adds the losses up.  Up to eight runs of one sequence are
+// one cluster, whose first block does that in the same launch (257 x 16: 4.3 us against 5.1 us, and 2.3 us less of
+// the host's time).
 //
 // A group of SUB lanes takes a token, VPL values to a lane; groups of a warp take neighbouring tokens.  Rows are
 // fetched an iteration ahead.  What bounds it: two special-function instructions to a sigmoid and one to an
 // exponential (16 a cycle and SM) and about 12 others to a value; with few tokens the chain of two launches.
-// Measured: 16384 x 128
-// fp32 softmax losses 9.4 us, gradient with a sum 5.4 us (25 MB: 4.7 TB/s); 65521 x 256 bf16 sigmoid losses of 29
-// sequences 23.8 us; gradient of 32749 x 250 bf16 sigmoid, 17 sequences, 13.6 us.
+// Measured: 16384 x 128 fp32 softmax losses 9.5 us, gradient with a sum 5.4 us (25 MB: 4.7 TB/s); 65521 x 256 bf16
+// sigmoid losses of 29 sequences 24 us; gradient of 32749 x 250 bf16 sigmoid, 17 sequences, 13.6 us.
 #include <limits.h>
 #include <math.h>
 
@@ -50,6 +51,7 @@ struct BalanceParams {
   RowSums* rows;  // [runs + B]
   float* part;    // [B][col_blocks], then [B] sums of lse^2
   unsigned* ticket;
+  bool alone;  // the grid is one cluster and needs no second kernel
   int32_t *counts, *stats;
   float *mean, *loss;
   uint32_t* status;
@@ -577,6 +579,35 @@ __global__ void __launch_bounds__(run_threads(VPL), 2) balance_kernel(const Bala
       if (lane == 0) p.rows[row] = r;
     }
   }
+  if (!p.alone) return;
+  // one sequence, a row to each block
+  cluster_sync_all();
+  if (blockIdx.x != 0) return;
+  RowSums all{0, 0, 0.0f, 0};
+  for (int r = 0; r < p.runs; ++r) all = all + p.rows[r];
+  float dot = 0.0f;
+  for (int e = threadIdx.x; e < E; e += THREADS) {
+    float s = 0.0f;
+    int n = 0;
+    for (int r = 0; r < p.runs; ++r) {
+      s += p.sums[(size_t)r * E + e];
+      n += p.hist[(size_t)r * E + e];
+    }
+    p.counts[e] = n;
+    p.mean[e] = all.tokens > 0 ? s / (float)all.tokens : 0.0f;
+    dot = fmaf((float)n, s, dot);
+  }
+  dot = group_sum<32>(dot);
+  if (lane == 0) smem[warp] = dot;  // the columns' sums have been read
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < WARPS; ++w) dot += smem[w];
+    p.stats[0] = p.stats[2] = all.tokens;
+    p.stats[1] = all.pairs;
+    p.stats[3] = all.tokens > 0;
+    p.loss[0] = all.pairs > 0 ? p.coef * (dot * ((float)E / ((float)all.pairs * (float)all.tokens))) : 0.0f;
+    p.loss[1] = all.tokens > 0 ? p.z_coef * (all.z / (float)all.tokens) : 0.0f;
+  }
 }
 
 // One block to COLS experts of a sequence: its pieces' rows are added in order.
@@ -848,7 +879,8 @@ template <lrmoe_dtype DT, bool SIGMOID, int VPL, int SUB, int G>
 struct Forward {
   static cudaError_t run(const BalanceParams& p, cudaStream_t s) {
     const size_t smem = sizeof(float) * (run_threads(VPL) / 32 + 1) * (size_t)p.E;  // 36 KB at most
-    return launch_pdl(balance_kernel<DT, SIGMOID, VPL, SUB, G>, dim3(p.runs), dim3(run_threads(VPL)), smem, s, p);
+    return launch_pdl_cluster(balance_kernel<DT, SIGMOID, VPL, SUB, G>, dim3(p.runs), dim3(run_threads(VPL)), smem, s,
+                              p.alone ? p.runs : 1, p);
   }
 };
 
@@ -921,13 +953,14 @@ cudaError_t launch_balance(const void* logits, int T, int E, lrmoe_dtype dt, con
   p.rows = reinterpret_cast<RowSums*>(w + q.rows);
   p.part = reinterpret_cast<float*>(w + q.part);
   p.ticket = reinterpret_cast<unsigned*>(w + q.ticket);
+  p.alone = off == nullptr && B == 1 && q.runs <= 8;
   p.counts = counts;
   p.stats = stats;
   p.mean = mean;
   p.loss = loss;
   p.status = status;
   cudaError_t e = by_type<Forward>(p, dt, fn == LRMOE_SCORE_SIGMOID, s);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.alone) return e;
   const unsigned blocks = (unsigned)((long long)B * q.col_blocks);
   if (q.cols == 64) return launch_pdl(balance_sum_kernel<64, 256>, dim3(blocks), dim3(256), 0, s, p);
   if (q.cols == 32) return launch_pdl(balance_sum_kernel<32, 1024>, dim3(blocks), dim3(1024), 0, s, p);
