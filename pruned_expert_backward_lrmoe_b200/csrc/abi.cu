@@ -752,6 +752,7 @@ static int check_balance(int T, int E, lrmoe_dtype dt, int k, lrmoe_score_fn sco
   REQUIRE(valid_score_fn(score_fn), "unknown score function %d", (int)score_fn);
   if (int r = check_pairs(T, k, E)) return r;
   if (E > kMaxGroupedExperts) return fail(LRMOE_ERR_UNSUPPORTED, "E=%d > %d", E, kMaxGroupedExperts);
+  REQUIRE(T <= 1 << 30, "T=%d > 2^30 is not supported", T);
   REQUIRE(B > 0 && (seq_offsets != nullptr || B == 1),
           "B=%d must be positive, and 1 without seq_offsets", B);
   REQUIRE((long long)B * E < (1LL << 31) - 1, "B*E overflows int32");

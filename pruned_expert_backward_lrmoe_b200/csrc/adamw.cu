@@ -230,7 +230,7 @@ __device__ __forceinline__ void scale_of(float top, float& scale, float& inv) {
 
 struct Hyper {
   F2 b1, a1, b2, a2;  // b and 1 - b, each twice
-  F2 eps;
+  F2 eps, one;
   float lr, rate, root;  // lr, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   double log_b1, log_b2;
   const float* lr_dev;
@@ -280,7 +280,8 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
 }
 
 // What a step computes of two values.  Each product and sum of m and v is rounded by itself: what is kept
-// in 8 bits depends on their last bits.
+// in 8 bits depends on their last bits.  The sums are written as products with a 1 that the compiler does not
+// know: it fuses a plain sum of pairs with the product before it.
 struct Step {
   F2 gs, root, rate, decay;  // rate and decay negative
   const Hyper& hy;
@@ -292,8 +293,8 @@ struct Step {
       v = v * vs;
       v = v * v;
     }
-    m1 = hy.b1 * m + hy.a1 * g;
-    v1 = hy.b2 * v + hy.a2 * g * g;
+    m1 = fma2(hy.a1 * g, hy.one, hy.b1 * m);
+    v1 = fma2(hy.a2 * g * g, hy.one, hy.b2 * v);
   }
   // the weights after the step, with r1 the root of v1
   __device__ __forceinline__ F2 weights(F2 p, F2 m1, F2 r1) const {
@@ -763,6 +764,7 @@ cudaError_t launch_adamw(const lrmoe_tensor* t, int count, lrmoe_dtype pdt, lrmo
   h.b2 = F2::twice((float)a.beta2);
   h.a2 = F2::twice((float)(1.0 - a.beta2));
   h.eps = F2::twice(a.eps);
+  h.one = F2::twice(1.0f);
   h.log_b1 = log(a.beta1);
   h.log_b2 = log(a.beta2);
   h.step = a.step < 1 ? 1 : a.step;

@@ -182,6 +182,30 @@ def test_step_and_rate_on_the_device():
         assert ((x - y).abs() <= 4 * U * x.abs() + 1e-2 * 4 * U).all()
 
 
+@pytest.mark.parametrize("n", [5000, 200])
+def test_products_and_sums_of_the_states_are_rounded_one_by_one(n):
+    """Bit for bit what elementary operations give: whether a value next to a border of its 8-bit code falls on one side
+    or the other hangs on the last bit."""
+    t = Tensors([(n,)], seed=12)
+    g, m, v = t.grads[0] * 0.5, t.state["m"][0].clone(), t.state["v"][0].clone()
+    b1, b2, a1, a2 = (torch.tensor(x, device="cuda") for x in (0.9, 0.95, 1 - 0.9, 1 - 0.95))
+    L.lrmoe_adamw(t.list, lr=1e-3, step=10, beta1=0.9, beta2=0.95, grad_scale=torch.tensor([0.5], device="cuda"))
+    x, y = b1 * m, a1 * g
+    m1 = x + y
+    x, y = b2 * v, a2 * g * g
+    v1 = x + y
+    assert torch.equal(t.state["m"][0], m1) and torch.equal(t.state["v"][0], v1)
+    # and from 8-bit states the scales, which show the largest of each block
+    e = Tensors([(n,)], bits=8, seed=12)
+    spread = lambda s: s.repeat_interleave(256)[:n]  # noqa: E731
+    m0 = e.state["m"][0].float() * spread(e.state["m_scale"][0])
+    v0 = (e.state["v"][0].float() * spread(e.state["v_scale"][0])).square()
+    L.lrmoe_adamw(e.list, lr=1e-3, step=10, beta1=0.9, beta2=0.95, grad_scale=torch.tensor([0.5], device="cuda"))
+    x, y = b1 * m0, a1 * (e.grads[0] * 0.5)
+    top = torch.nn.functional.pad((x + y).abs(), (0, -n % 256)).view(-1, 256).amax(1)
+    assert torch.equal(e.state["m_scale"][0], top * (1 / torch.tensor(448.0, device="cuda")))
+
+
 @pytest.mark.parametrize("beta1,beta2", [(0.0, 0.0), (0.9, 0.0), (0.0, 0.999), (0.9999, 0.99999)])
 def test_betas(beta1, beta2):
     t = Tensors([(3000,), (17,)])
@@ -325,7 +349,8 @@ def norm_of(tensors, max_norm=math.inf):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("shapes", [[(1,)], [(0,)], [(0,), (0, 4)], [(5,), (0,), (2049,)], SHAPES, [(1000, 3001)]])
+@pytest.mark.parametrize("shapes", [[(1,)], [(0,)], [(0,), (0, 4)], [(5,), (0,), (2049,)], SHAPES, [(1000, 3001)],
+                                    [(32 * 2048,)], [(32 * 2048 + 1,)], [(7,)] * 32, [(7,)] * 33, [(4 * 2048,)], [(4 * 2048 + 1,)]])
 def test_norm(shapes, dt):
     g = torch.Generator(device="cuda").manual_seed(1)
     ts = [torch.randn(s, generator=g, device="cuda").to(TYPE[dt]) for s in shapes]

@@ -4,7 +4,7 @@ Tolerances (u = 2^-24): an exponential of d = z - max is within (4 |d| + 4) u of
 product with log2 e and that constant are rounded, ex2.approx is good to 2^-22), a sum of it and at most
 1024 others adds 37 additions, the quotient 4 more: a share is within K = 8 d + 100 of itself, twice that
 where sigmoids and 1 - sigmoid are multiplied.  Sums over tokens: a run's tokens go to 8 warps and those to
-at most 592 runs, each a chain of additions: depth = run + 8 + 592 / 4 + 64.  lse is within (K + 4 |zmax|) u.
+at most 592 runs, each a chain of additions: depth = run + 8 + 592 / 4 + 64 (16 warps and 296 runs take fewer).  lse is within (K + 4 |zmax|) u.
 """
 import numpy as np
 import pytest
@@ -162,6 +162,33 @@ def test_sequences(T, E, k, which, kind, dt):
     c.check_grad(dz, kind, 2.0, 0.1)
     assert int(c.status.item()) == ref["status"]           # what lies behind the sequences is not read
     assert not dz[:lo].any() and not dz[hi:].any()
+
+
+@pytest.mark.parametrize("T,E,k", [(1024, 16, 2), (1025, 16, 2), (256, 128, 8), (257, 128, 8), (128, 256, 4), (129, 256, 4),
+                                   (70, 600, 3), (18944, 32, 2), (18945, 128, 2)])
+def test_one_sequence_given_by_its_bounds(T, E, k):
+    """The same tokens as one sequence without and with bounds: a single launch or two, runs added by one block or more."""
+    c = Case(T, E, k, "f32", seed=6, masks=False)
+    a = c.forward(c.outputs(), "softmax", 1.5, 0.2)
+    c.check_forward(a, "softmax", 1.5, 0.2)
+    c.offt = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    b = c.forward(c.outputs(), "softmax", 1.5, 0.2)
+    c.check_forward(b, "softmax", 1.5, 0.2)
+    assert torch.equal(a["counts"], b["counts"]) and torch.equal(a["stats"], b["stats"])
+    for n in ("mean_score", "loss"):  # at most the order of the runs' sums differs
+        assert ((a[n] - b[n]).abs() <= 300 * U * a[n].abs()).all()
+
+
+@pytest.mark.parametrize("kind,dt", [("softmax", "f32"), ("sigmoid", "bf16")])
+def test_long_runs(kind, dt):
+    """Runs and warps with more tokens than they look at at a time, cut by sequences."""
+    T = 200001
+    c = Case(T, 8, 2, dt, off=[3, 70000, 70001, 130001, T - 5], seed=9, masks=False)
+    c.idxn[::7] = -1
+    c.idx.copy_(torch.from_numpy(c.idxn))
+    out = c.forward(c.outputs(), kind, 1.0, 0.5)
+    c.check_forward(out, kind, 1.0, 0.5)
+    c.check_grad(c.grad(out, kind, 1.0, 0.5), kind, 1.0, 0.5)
 
 
 def test_many_short_sequences():

@@ -128,6 +128,9 @@ def test_balance_refuses(lib):
     for at, value in ((1, 0), (1, -1), (2, 0), (5, 0), (5, 33), (3, 7), (6, 2), (8, 0), (9, float("inf")), (9, float("nan")),
                       (10, float("inf")), (8, 2 ** 28)):
         refused(at, value, b"")
+    one = list(ok)
+    one[1], one[5] = 2 ** 30 + 1, 1
+    assert lib.lrmoe_balance(*one) == L.LRMOE_ERR_INVALID_ARG and b"2^30" in lib.lrmoe_last_error()
     refused(2, 1025, b"1024", L.LRMOE_ERR_UNSUPPORTED)
     refused(15, NULL, b"workspace", L.LRMOE_ERR_WORKSPACE)
     refused(16, need - 1, b"workspace", L.LRMOE_ERR_WORKSPACE)
