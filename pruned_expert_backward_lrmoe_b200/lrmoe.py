@@ -8,6 +8,7 @@ If the library is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional
 
@@ -546,6 +547,16 @@ def lrmoe_balance_grad(logits, topk_idx, counts, stats, dlogits, seq_offsets=Non
                                      c, st, dl, ad, dz, _status(status, dev), _launch(dev, stream)))
 
 
+@functools.lru_cache(maxsize=None)
+def _tensor_dtype():
+    """numpy's view of lrmoe_tensor."""
+    import numpy as np
+    kinds = {"n": np.int64, "weight_decay": np.float32}
+    names = [n for n, _ in lrmoe_tensor._fields_]
+    return np.dtype({"names": names, "formats": [kinds.get(n, np.uint64) for n in names],
+                     "offsets": [getattr(lrmoe_tensor, n).offset for n in names], "itemsize": ctypes.sizeof(lrmoe_tensor)})
+
+
 class TensorList:
     """The tensors of lrmoe_grad_norm and lrmoe_adamw, checked once and kept: gradients and, for a
     step, parameters, states m and v (lists of the same length; see alloc_adamw), their scales for
@@ -585,23 +596,35 @@ class TensorList:
             else [float(w) for w in weight_decay]
         if len(decay) != self.count:
             raise ValueError(f"weight_decay: {len(decay)} values, {self.count} tensors")
+        import numpy as np
         self.tensors = (lrmoe_tensor * self.count)()
-        written = []  # (first, past the last address, name), of what a step writes and reads
-        for i, g in enumerate(grads):
-            t = self.tensors[i]
-            t.n, t.weight_decay = g.numel(), decay[i]
-            for name, ts in given.items():
-                if ts is None:
-                    continue
-                shape = (-(-t.n // 256),) if name.endswith("_scale") else g.shape
-                at = _arg(f"{name} {i}", ts[i], types[name], shape, self.device)
-                setattr(t, name, at)
-                if t.n and params is not None:
-                    written.append((at, at + ts[i].numel() * ts[i].element_size(), f"{name} {i}"))
-        written.sort()
-        for a, b in zip(written, written[1:]):
-            if b[0] < a[1]:
-                raise ValueError(f"{a[2]} and {b[2]} overlap")
+        view = np.frombuffer(self.tensors, _tensor_dtype())
+        shapes = [g.shape for g in grads]
+        n = view["n"][:] = np.array([g.numel() for g in grads], np.int64)
+        view["weight_decay"] = decay
+        scales = [(b,) for b in (-(-n // 256)).tolist()] if self.state_bits == 8 else None
+        starts, ends, names = [], [], []
+        for name, ts in given.items():
+            if ts is None:
+                continue
+            dtype, dev = types[name], self.device
+            view[name] = at = np.array([
+                _arg(f"{name} {i}", t, dtype, shape, dev)
+                if t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous()
+                else t.data_ptr()
+                for i, (t, shape) in enumerate(zip(ts, scales if name.endswith("_scale") else shapes))], np.uint64)
+            starts.append(at)
+            ends.append(at + (-(-n // 256) if name.endswith("_scale") else n).astype(np.uint64)
+                        * np.uint64(ts[0].element_size()))
+            names.append(name)
+        if params is not None:  # what a step writes and reads
+            starts, ends = np.concatenate(starts), np.concatenate(ends)
+            order = np.flatnonzero(ends > starts)
+            order = order[np.argsort(starts[order], kind="stable")]
+            clash = np.flatnonzero(starts[order][1:] < ends[order][:-1])
+            if clash.size:
+                a, b = (f"{names[j // self.count]} {j % self.count}" for j in order[clash[0]:clash[0] + 2].tolist())
+                raise ValueError(f"{a} and {b} overlap")
         self.kept = given  # the memory stays while the list does
 
 
