@@ -7,11 +7,16 @@
 //
 // The list of tensors travels in the launch's parameters, so that a call needs no device memory for it
 // and a captured call keeps its own.  Tiles of 2048 values are dealt to the blocks in turn; a warp takes
-// 256 neighbouring values of a tile, lane l the values 4 l .. 4 l + 3 of each half.  That is the block of
-// the 8-bit states, whose largest magnitudes are then one reduction over the warp.
+// 256 neighbouring values of a tile.  That is the block of the 8-bit states, whose largest magnitudes are then
+// one reduction over the warp.
 //
-// HBM-bound: every value is read and written once.
+// Every value is read and written once.  Bound by HBM: the norm (604 M fp32 values: 333 us, 7.3 TB/s) and the step
+// with 32-bit states (with bf16 weights and copies 2.78 ms, 6.5 TB/s).  With 8-bit states 12 bytes a value are
+// few beside the 60 instructions that decode, step, draw and encode it: 1.45 ms, 5.0 TB/s, which is why whole
+// blocks take a path of their own, in pairs of values.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -212,6 +217,19 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   return h ^ (h >> 16);
 }
 
+// The same with its upper half by itself, which the last step of mix leaves as it is.
+struct Word {
+  uint32_t w, high;
+};
+__device__ __forceinline__ Word mix_word(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x9E3779B1u;
+  h ^= h >> 15;
+  h *= 0x6A09E667u;
+  const uint32_t high = h >> 16;
+  return Word{h ^ high, high};
+}
+
 __device__ __forceinline__ float rcp_fast(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -345,14 +363,14 @@ __device__ __forceinline__ unsigned short m_codes(F2 m, F2 im, uint32_t w0, uint
 
 // SMALL: there may be roots below the smallest code: those become it, but for 0.
 template <bool SMALL>
-__device__ __forceinline__ unsigned short r_codes(F2 r, F2 iv, uint32_t w0, uint32_t w1) {
+__device__ __forceinline__ unsigned short r_codes(F2 r, F2 iv, uint32_t w0, uint32_t w1 /* 16 bits */) {
   const F2 y = r * iv;
   float a = y.x(), c = y.y();
   if (SMALL) {
     a = r.x() > 0.0f ? fmaxf(a, kDown * 0.001953125f) : 0.0f;
     c = r.y() > 0.0f ? fmaxf(c, kDown * 0.001953125f) : 0.0f;
   }
-  return codes_of(F2(__uint_as_float(round_bits(a, w0 >> 16)), __uint_as_float(round_bits(c, w1 >> 16))) * F2(kUp));
+  return codes_of(F2(__uint_as_float(round_bits(a, w0)), __uint_as_float(round_bits(c, w1))) * F2(kUp));
 }
 
 // bf16 bits of p in the high half, by the random bits of w
@@ -491,20 +509,19 @@ struct Block {
       scale_of(top_m, sm, im);
       scale_of(top_r, sv, iv);
     }
-    uint32_t w[8];
-    if constexpr (kRandom) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = mix(key + (uint32_t)(i / 4 * kHalf + i % 4));
-    }
     if constexpr (MASTER) store<LRMOE_F32>(at.master, p1);
-    if constexpr (kRandomParam) {
+    if constexpr (!kRandomParam) store<PDT>(at.p, p1);
+    auto bf16_pair = [&](int i, uint32_t a, uint32_t b) {
+      return __byte_perm(random_bf16(p1[i].x(), a), random_bf16(p1[i].y(), b), 0x7632);
+    };
+    if constexpr (kRandomParam && BITS == 32) {
       uint32_t b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        b[i] = __byte_perm(random_bf16(p1[i].x(), w[2 * i]), random_bf16(p1[i].y(), w[2 * i + 1]), 0x7632);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t at0 = key + (uint32_t)(i / 2 * kHalf + i % 2 * 2);
+        b[i] = bf16_pair(i, mix(at0), mix(at0 + 1));
+      }
       store_halves(at.p, b);
-    } else {
-      store<PDT>(at.p, p1);
     }
     if constexpr (BITS == 32) {
       store<LRMOE_F32>(at.m, m1);
@@ -515,18 +532,24 @@ struct Block {
         *at.v_scale = sv;
       }
       const F2 fm(im * kDown), fv(iv * kDown);
-      uint32_t q[4];
+      auto codes = [&](auto small) {
+        uint32_t mq[4], vq[4];
+        [[maybe_unused]] uint32_t b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = m_codes(m1[i], fm, w[2 * i], w[2 * i + 1]);
-      *reinterpret_cast<uint2*>(at.m) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-      if (__all_sync(kFull, least * iv >= 0.001953125f)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = r_codes<false>(r1[i], fv, w[2 * i], w[2 * i + 1]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = r_codes<true>(r1[i], fv, w[2 * i], w[2 * i + 1]);
-      }
-      *reinterpret_cast<uint2*>(at.v) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+        for (int i = 0; i < 4; ++i) {
+          const Word w0 = mix_word(key + (uint32_t)(2 * i)), w1 = mix_word(key + (uint32_t)(2 * i + 1));
+          mq[i] = m_codes(m1[i], fm, w0.w, w1.w);
+          vq[i] = r_codes<decltype(small)::value>(r1[i], fv, w0.high, w1.high);
+          if constexpr (kRandomParam) b[i] = bf16_pair(i, w0.w, w1.w);
+        }
+        *reinterpret_cast<uint2*>(at.m) = make_uint2(mq[0] | (mq[1] << 16), mq[2] | (mq[3] << 16));
+        *reinterpret_cast<uint2*>(at.v) = make_uint2(vq[0] | (vq[1] << 16), vq[2] | (vq[3] << 16));
+        if constexpr (kRandomParam) store_halves(at.p, b);
+      };
+      if (__all_sync(kFull, least * iv >= 0.001953125f))
+        codes(std::false_type());
+      else
+        codes(std::true_type());
     }
     return true;
   }
@@ -587,7 +610,7 @@ struct Block {
           // in two steps: the inverse scale times 2^-120 may be no normal number
           const unsigned short mq = m_codes(F2(m[h][j]) * F2(im), F2(kDown), w, w);
           const float x = v[h][j] * iv;
-          const unsigned short vq = r_codes<true>(F2(v[h][j] > 0.0f ? fmaxf(x, 0.001953125f) : 0.0f), F2(kDown), w, w);
+          const unsigned short vq = r_codes<true>(F2(v[h][j] > 0.0f ? fmaxf(x, 0.001953125f) : 0.0f), F2(kDown), w >> 16, w >> 16);
           if (j < left) {
             static_cast<uint8_t*>(it.m)[i + j] = (uint8_t)mq;
             static_cast<uint8_t*>(it.v)[i + j] = (uint8_t)vq;
@@ -784,6 +807,8 @@ cudaError_t launch_adamw(const lrmoe_tensor* t, int count, lrmoe_dtype pdt, lrmo
     auto kern = pdt == LRMOE_F32 ? pick<LRMOE_F32, false, CAP>(gdt, bits)
                 : master         ? pick<LRMOE_BF16, true, CAP>(gdt, bits)
                                  : pick<LRMOE_BF16, false, CAP>(gdt, bits);
+    // 32 blocks to an SM, of which 3 or 4 fit: shorter last rounds (604 M values with 8, 16, 32: 2.84, 2.83, 2.83 ms with
+    // 32-bit states, 1.75, 1.72, 1.71 ms with 8-bit ones before the short path)
     return launch_pdl(kern, dim3(grid_of(list, items, 32)), dim3(kThreads), 0, s, list, items, h);
   });
 }
