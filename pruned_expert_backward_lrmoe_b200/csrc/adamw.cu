@@ -33,7 +33,7 @@ constexpr int kNormBlocks = 148 * 8; // at most, of a launch
 // less of the host's time; 32 tiles 2.8 against 2.6 us, 128 tiles 4.4 against 2.6 us).
 constexpr unsigned kNormAlone = 32;
 
-constexpr int kFew = 24, kMany = 448;  // tensors of a launch: 1.8 KB or 32 KB of parameters
+constexpr int kFew = 24, kSome = 112, kMany = 448;  // tensors of a launch: 1.8, 8 or 32 KB of parameters
 
 struct Item {
   void* p;
@@ -715,15 +715,21 @@ template <typename F>
 cudaError_t over_launches(const lrmoe_tensor* t, int count, F&& f) {
   int next = 0, first = 0;
   while (next < count) {
-    cudaError_t e;
-    if (count - next <= kFew) {
-      Items<kFew> list;
+    auto part = [&](auto& list) {
       const int n = fill(list, t, count, next, first);
-      e = list.t[n - 1].end ? f(list, n, first) : cudaSuccess;
+      return list.t[n - 1].end ? f(list, n, first) : cudaSuccess;
+    };
+    const int left = count - next;
+    cudaError_t e;
+    if (left <= kFew) {
+      Items<kFew> list;
+      e = part(list);
+    } else if (left <= kSome) {
+      Items<kSome> list;
+      e = part(list);
     } else {
       Items<kMany> list;
-      const int n = fill(list, t, count, next, first);
-      e = list.t[n - 1].end ? f(list, n, first) : cudaSuccess;
+      e = part(list);
     }
     if (e != cudaSuccess) return e;
   }

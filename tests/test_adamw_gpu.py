@@ -147,7 +147,7 @@ def test_first_step_from_nothing(bits):
         assert (np.abs(moved - HYPER["lr"] * np.sign(a["grad"]))[big] <= 1.1e-2 * HYPER["lr"]).all()
 
 
-@pytest.mark.parametrize("count", [1, 24, 25, 448, 449, 1000])
+@pytest.mark.parametrize("count", [1, 24, 25, 112, 113, 448, 449, 1000])
 @pytest.mark.parametrize("bits", [32, 8])
 def test_many_tensors(count, bits):
     """More tensors than fit a launch; each of its own size, empty ones among them."""
